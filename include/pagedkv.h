@@ -84,7 +84,10 @@ typedef enum {
     PKV_KERNEL_APPEND = 1,
     PKV_KERNEL_COPY_BLOCKS = 2,
     PKV_KERNEL_SWAP_BLOCKS = 3,
-    PKV_KERNEL_KINDS = 4
+    PKV_KERNEL_PREFILL = 4,
+    PKV_KERNEL_TREE = 5,
+    PKV_KERNEL_QK_ROPE = 6,
+    PKV_KERNEL_KINDS = 7
 } pkv_kernel_kind;
 
 /*
@@ -230,6 +233,123 @@ PKV_API size_t paged_attention_workspace_size(int num_seqs, int num_heads, int m
 PKV_API int kv_cache_append(void* k_cache, void* v_cache, const void* k, const void* v,
                     const int64_t* slot_mapping, int num_tokens, int num_kv_heads, int head_dim,
                     int block_size, int num_blocks, int dtype, void* stream);
+
+/*
+ * The step between the q/k/v projection and the attention, in one pass:
+ * per-head RMS norm of q and k, position rotation of both, and the append of
+ * k and v into their slots.  The pages have no counterpart of this call (nor
+ * of the prompt and drafted-tree attention below): they describe the cache,
+ * not the layer around it.  For token t and each of its heads x of q or k:
+ *     x' = x / sqrt(mean(x^2) + eps) * weight     (weight NULL: x' = x)
+ *     angle_i = positions[axis(i)][t] * inv_freq[i],  0 <= i < R / 2
+ *     (x'_p, x'_r) -> (x'_p cos - x'_r sin, x'_r cos + x'_p sin)
+ * with (p, r) = (i, i + R / 2), or (2i, 2i + 1) when `interleaved`; dims from
+ * R on keep x'.  fp32 arithmetic, angles reduced in fp64 (any int32 position),
+ * one rounding to the output's type.  q goes to q_out, k and v (v as it is)
+ * to slot slot_mapping[t] as in kv_cache_append: slot < 0 stores no k and v
+ * (q_out is still written); slots past the pool are device faults.
+ *   q, q_out    [num_tokens][num_heads][head_dim], k, v [num_tokens]
+ *               [num_kv_heads][head_dim]; the strides are elements between two
+ *               tokens, so all may be slices of one projection output
+ *               (multiples of 16 bytes; heads of a token adjacent).  q_out may
+ *               be q itself; it must not overlap anything else.
+ *   positions   int32 [num_sections][num_tokens]; negative ones rotate back.
+ *   inv_freq    float [R / 2].
+ *   q_weight, k_weight  [head_dim] of `dtype`, or NULL.
+ *   sections    host array: number of frequencies i of each position axis, in
+ *               order (one axis: {R / 2}; time, height, width: three numbers).
+ *               Their sum is R / 2, a multiple of 8, R <= head_dim; at most 4.
+ * head_dim 64 or 128; any numbers of heads and block sizes.
+ */
+PKV_API int qk_norm_rope_append(void* q_out, const void* q, const void* k, const void* v, void* k_cache,
+                                void* v_cache, const int64_t* slot_mapping, const int32_t* positions,
+                                const float* inv_freq, const void* q_weight, const void* k_weight, float eps,
+                                const int* sections, int num_sections, int interleaved, long long q_out_stride,
+                                long long q_stride, long long k_stride, long long v_stride, int num_tokens,
+                                int num_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                                int dtype, void* stream);
+
+/* The same with fp8 pools: q, k, v and the weights bf16, k and v stored as the
+ * e4m3 codes of value / scale as in kv_cache_append_fp8 (k rounded once, from
+ * its fp32 value). */
+PKV_API int qk_norm_rope_append_fp8(void* q_out, const void* q, const void* k, const void* v, void* k_cache,
+                                    void* v_cache, const float* k_scales, const float* v_scales,
+                                    const int64_t* slot_mapping, const int32_t* positions, const float* inv_freq,
+                                    const void* q_weight, const void* k_weight, float eps, const int* sections,
+                                    int num_sections, int interleaved, long long q_out_stride, long long q_stride,
+                                    long long k_stride, long long v_stride, int num_tokens, int num_heads,
+                                    int num_kv_heads, int head_dim, int block_size, int num_blocks, void* stream);
+
+/*
+ * Causal attention of whole prompts, or chunks of them, over the paged cache.
+ * The queries of sequence s are rows query_start[s] .. query_start[s + 1] - 1
+ * of q and out (n of them; 0 is allowed): the last n of its context_lens[s]
+ * tokens, whose K and V are in the cache already (kv_cache_append or
+ * qk_norm_rope_append of the same step).  The i-th of them attends keys
+ * 0 .. context_lens[s] - n + i.
+ *   query_start  int32 [num_seqs + 1], not decreasing, from 0.  Rows from
+ *                query_start[num_seqs] to num_tokens, which pad the batch, are
+ *                neither read nor written.
+ *   q            [num_tokens][num_heads][head_dim], q_stride elements between
+ *                two tokens (a multiple of 16 bytes); out is contiguous.
+ *   workspace    at least paged_attention_prefill_workspace_size bytes,
+ *                256-byte aligned, zero-filled once before its first use and
+ *                left ready for the next call (of any shape, tree attention
+ *                included).  Two calls in flight at once, captured graphs
+ *                included, must not share one, nor share it with a decode.
+ * Otherwise as paged_attention_decode_ex.  A sequence with fewer context
+ * tokens than queries, a context past its table, or rows outside q is a device
+ * fault; its rows inside q become zeros.  A key that a row does not see has no
+ * part in it, whatever its K and V hold.  One launch.
+ */
+PKV_API int paged_attention_prefill(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                    const int32_t* block_tables, const int32_t* context_lens,
+                                    const int32_t* query_start, long long q_stride, int num_tokens, int num_seqs,
+                                    int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                    int max_blocks_per_seq, float scale, int num_blocks, int dtype, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/* The same over an fp8 cache (scales as in paged_attention_decode_fp8; q and
+ * out bf16). */
+PKV_API int paged_attention_prefill_fp8(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                        const float* k_scales, const float* v_scales, const int32_t* block_tables,
+                                        const int32_t* context_lens, const int32_t* query_start, long long q_stride,
+                                        int num_tokens, int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                        int block_size, int max_blocks_per_seq, float scale, int num_blocks,
+                                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Attention of a tree of drafted tokens over the paged cache (the check of a
+ * speculative step).  As paged_attention_prefill, with the n queries of a
+ * sequence its drafts: their K and V are the last n of its context_lens[s]
+ * tokens in the cache, in the same order, and draft i attends every committed
+ * token (keys 0 .. context_lens[s] - n - 1), itself and its ancestors.
+ *   parents      int32 [num_tokens]: index within the sequence's drafts of each
+ *                draft's parent, smaller than its own, or -1 (the parent is the
+ *                last committed token).  Others are device faults; such a
+ *                draft's walk ends there.
+ * A chain (parents i - 1) is paged_attention_prefill.
+ */
+PKV_API int paged_attention_tree(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                 const int32_t* block_tables, const int32_t* context_lens,
+                                 const int32_t* query_start, const int32_t* parents, long long q_stride,
+                                 int num_tokens, int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                 int block_size, int max_blocks_per_seq, float scale, int num_blocks, int dtype,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+PKV_API int paged_attention_tree_fp8(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                     const float* k_scales, const float* v_scales, const int32_t* block_tables,
+                                     const int32_t* context_lens, const int32_t* query_start, const int32_t* parents,
+                                     long long q_stride, int num_tokens, int num_seqs, int num_heads,
+                                     int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
+                                     float scale, int num_blocks, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
+/* Bytes of workspace of the prompt and drafted-tree calls, for caches of type
+ * cache_dtype; 0 on bad sizes.  Grows with num_tokens up to a full tile's
+ * rows, then no more. */
+PKV_API size_t paged_attention_prefill_workspace_size(int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                                                      int cache_dtype);
 
 /*
  * Copy-on-write block copy ("Sharing blocks between sequences": the writer's

@@ -13,6 +13,7 @@
 #include <vector>
 
 #include "../../include/pagedkv.h"
+#include "attn_launch.h"
 #include "kv_ops.cuh"
 #include "launch.h"
 #include "plan.cuh"
@@ -433,6 +434,162 @@ int decode_impl(void* out, const void* q, const void* k_cache, const void* v_cac
 
 }  // namespace
 
+namespace {
+
+// Workspace of the multi-query attention: one counter per CTA of the grid
+// (zero between launches), then the partial results, two per CTA.
+struct AttnLayout {
+    pkv::AttnShape shape;
+    int part_rows;
+    size_t ml_off, o_off, total;
+};
+
+AttnLayout attn_layout(long long num_tokens, long long group, long long D, int kv_dtype) {
+    AttnLayout w;
+    w.shape = pkv::attn_shape(kv_dtype);
+    w.part_rows = num_tokens * group < w.shape.rows ? (int)(num_tokens * group) : w.shape.rows;
+    const size_t rows = size_t(2) * w.shape.grid * w.part_rows;
+    w.ml_off = align256(w.shape.grid * sizeof(int));
+    w.o_off = w.ml_off + align256(rows * sizeof(float2));
+    w.total = w.o_off + align256(rows * D * sizeof(float));
+    return w;
+}
+
+// Shared body of prompt attention (parents null) and drafted-tree attention.
+int attn_impl(int kind, void* out, const void* q, const void* k_cache, const void* v_cache, const float* k_scales,
+              const float* v_scales, const int32_t* block_tables, const int32_t* context_lens,
+              const int32_t* query_start, const int32_t* parents, long long q_stride, int num_tokens, int num_seqs,
+              int num_heads, int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq, float scale,
+              int num_blocks, int dtype, int kv_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    if (num_seqs < 0 || num_tokens < 0) return PKV_ERR_INVALID;
+    if (num_seqs == 0 || num_tokens == 0) return PKV_OK;
+    if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !query_start) return PKV_ERR_NULL;
+    if (num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads != 0) return PKV_ERR_INVALID;
+    if (head_dim <= 0 || block_size <= 0 || max_blocks_per_seq <= 0 || num_blocks <= 0) return PKV_ERR_INVALID;
+    if (dtype != PKV_F32 && dtype != PKV_BF16) return PKV_ERR_INVALID;
+    const bool fp8 = kv_dtype == PKV_FP8_E4M3;
+    if (fp8 && (!k_scales || !v_scales)) return PKV_ERR_NULL;
+    if (!isfinite(scale)) return PKV_ERR_INVALID;
+    const int group = num_heads / num_kv_heads;
+    if (!decode_shape_supported(head_dim, block_size, group)) return PKV_ERR_UNSUPPORTED;
+    if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache)) return PKV_ERR_INVALID;
+    if (q_stride < (long long)num_heads * head_dim || q_stride * elt_bytes(dtype) % 16 != 0) return PKV_ERR_INVALID;
+    if ((long long)max_blocks_per_seq * block_size > INT_MAX - 1024) return PKV_ERR_INVALID;
+    const AttnLayout w = attn_layout(num_tokens, group, head_dim, kv_dtype);
+    if (workspace == nullptr || workspace_bytes < w.total || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return PKV_ERR_WORKSPACE;
+    int dev = 0;
+    if (current_device(&dev) != PKV_OK) return PKV_ERR_CUDA;
+    int* err = nullptr;
+    if (error_word(dev, &err) != PKV_OK) return PKV_ERR_CUDA;
+    char* ws = static_cast<char*>(workspace);
+    pkv::AttnParams p;
+    p.out = out;
+    p.q = q;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.query_start = query_start;
+    p.parents = parents;
+    p.k_scales = k_scales;
+    p.v_scales = v_scales;
+    p.counters = reinterpret_cast<int*>(ws);
+    p.ws_ml = reinterpret_cast<float2*>(ws + w.ml_off);
+    p.ws_o = reinterpret_cast<float*>(ws + w.o_off);
+    p.err = err;
+    p.q_stride = q_stride;
+    p.num_seqs = num_seqs;
+    p.num_tokens = num_tokens;
+    p.num_heads = num_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.group_log2 = group == 1 ? 0 : group == 2 ? 1 : group == 4 ? 2 : 3;
+    p.block_size = block_size;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.num_blocks = num_blocks;
+    p.part_rows = w.part_rows;
+    p.qscale = scale * 1.4426950408889634f;  // log2(e): softmax runs in base 2
+    p.wait_ns = g_wait_ns.load();
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return launch(kind, st, [&] { return pkv::launch_attn(p, dtype, kv_dtype, head_dim, st); });
+}
+
+int rope_impl(void* q_out, const void* q, const void* k, const void* v, void* k_cache, void* v_cache,
+              const float* k_scales, const float* v_scales, const int64_t* slot_mapping, const int32_t* positions,
+              const float* inv_freq, const void* q_weight, const void* k_weight, float eps, const int* sections,
+              int num_sections, int interleaved, long long q_out_stride, long long q_stride, long long k_stride,
+              long long v_stride, int num_tokens, int num_heads, int num_kv_heads, int head_dim, int block_size,
+              int num_blocks, int dtype, bool fp8, void* stream) {
+    if (num_tokens < 0) return PKV_ERR_INVALID;
+    if (num_tokens == 0) return PKV_OK;
+    if (!q_out || !q || !k || !v || !k_cache || !v_cache || !slot_mapping || !positions || !inv_freq || !sections)
+        return PKV_ERR_NULL;
+    if (num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || num_blocks <= 0)
+        return PKV_ERR_INVALID;
+    if ((long long)num_heads + 2LL * num_kv_heads > INT_MAX / (head_dim > 256 ? head_dim : 256))
+        return PKV_ERR_INVALID;
+    if (dtype != PKV_F32 && dtype != PKV_BF16) return PKV_ERR_INVALID;
+    if (!(eps >= 0.f) || !isfinite(eps)) return PKV_ERR_INVALID;
+    if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
+    if (num_sections < 1) return PKV_ERR_INVALID;
+    if (num_sections > pkv::kRopeMaxAxes) return PKV_ERR_UNSUPPORTED;
+    long long pairs = 0;
+    for (int a = 0; a < num_sections; ++a) {
+        if (sections[a] < 0) return PKV_ERR_INVALID;
+        pairs += sections[a];
+    }
+    if (pairs <= 0 || 2 * pairs > head_dim) return PKV_ERR_INVALID;
+    if (pairs % 8 != 0) return PKV_ERR_UNSUPPORTED;
+    const int eb = elt_bytes(dtype);
+    const void* ptrs[] = {q_out, q, k, v, k_cache, v_cache, q_weight, k_weight};
+    for (const void* x : ptrs)
+        if (!aligned16(x)) return PKV_ERR_INVALID;
+    const long long strides[] = {q_out_stride, q_stride, k_stride, v_stride};
+    for (int i = 0; i < 4; ++i)
+        if (strides[i] < (long long)(i < 2 ? num_heads : num_kv_heads) * head_dim || strides[i] * eb % 16 != 0)
+            return PKV_ERR_INVALID;
+    int dev = 0;
+    if (current_device(&dev) != PKV_OK) return PKV_ERR_CUDA;
+    int* err = nullptr;
+    if (error_word(dev, &err) != PKV_OK) return PKV_ERR_CUDA;
+    pkv::RopeParams p;
+    p.q_out = q_out;
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.k_scales = k_scales;
+    p.v_scales = v_scales;
+    p.slot_mapping = slot_mapping;
+    p.positions = positions;
+    p.inv_freq = inv_freq;
+    p.q_weight = q_weight;
+    p.k_weight = k_weight;
+    p.err = err;
+    p.q_out_stride = q_out_stride;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.num_slots = (long long)num_blocks * block_size;
+    p.num_tokens = num_tokens;
+    p.num_heads = num_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.block_size = block_size;
+    p.pairs = (int)pairs;
+    int end = 0;
+    for (int a = 0; a < pkv::kRopeMaxAxes; ++a) {
+        if (a < num_sections) end += sections[a];
+        p.axis_end[a] = a + 1 < num_sections ? end : INT_MAX;
+    }
+    p.eps = eps;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return launch(PKV_KERNEL_QK_ROPE, st,
+                  [&] { return pkv::launch_qk_rope(p, dtype, fp8, interleaved != 0, head_dim, st); });
+}
+
+}  // namespace
+
 extern "C" {
 
 int paged_attention_decode_ex(void* out, const void* q, const void* k_cache, const void* v_cache,
@@ -586,6 +743,87 @@ int kv_cache_append_fp8(void* k_cache, void* v_cache, const float* k_scales,
         pkv::kv_append_fp8_kernel<<<(unsigned)blocks, 256, 0, st>>>(p);
         return cudaGetLastError();
     });
+}
+
+size_t paged_attention_prefill_workspace_size(int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                                              int cache_dtype) {
+    if (num_tokens <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads != 0 || head_dim <= 0 ||
+        !known_dtype(cache_dtype))
+        return 0;
+    return attn_layout(num_tokens, num_heads / num_kv_heads, head_dim, cache_dtype).total;
+}
+
+int paged_attention_prefill(void* out, const void* q, const void* k_cache, const void* v_cache,
+                            const int32_t* block_tables, const int32_t* context_lens, const int32_t* query_start,
+                            long long q_stride, int num_tokens, int num_seqs, int num_heads, int num_kv_heads,
+                            int head_dim, int block_size, int max_blocks_per_seq, float scale, int num_blocks,
+                            int dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    return attn_impl(PKV_KERNEL_PREFILL, out, q, k_cache, v_cache, nullptr, nullptr, block_tables, context_lens,
+                     query_start, nullptr, q_stride, num_tokens, num_seqs, num_heads, num_kv_heads, head_dim,
+                     block_size, max_blocks_per_seq, scale, num_blocks, dtype, dtype, workspace, workspace_bytes,
+                     stream);
+}
+
+int paged_attention_prefill_fp8(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                const float* k_scales, const float* v_scales, const int32_t* block_tables,
+                                const int32_t* context_lens, const int32_t* query_start, long long q_stride,
+                                int num_tokens, int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                int block_size, int max_blocks_per_seq, float scale, int num_blocks,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+    return attn_impl(PKV_KERNEL_PREFILL, out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                     query_start, nullptr, q_stride, num_tokens, num_seqs, num_heads, num_kv_heads, head_dim,
+                     block_size, max_blocks_per_seq, scale, num_blocks, PKV_BF16, PKV_FP8_E4M3, workspace,
+                     workspace_bytes, stream);
+}
+
+int paged_attention_tree(void* out, const void* q, const void* k_cache, const void* v_cache,
+                         const int32_t* block_tables, const int32_t* context_lens, const int32_t* query_start,
+                         const int32_t* parents, long long q_stride, int num_tokens, int num_seqs, int num_heads,
+                         int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq, float scale,
+                         int num_blocks, int dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    if (num_seqs > 0 && num_tokens > 0 && !parents) return PKV_ERR_NULL;
+    return attn_impl(PKV_KERNEL_TREE, out, q, k_cache, v_cache, nullptr, nullptr, block_tables, context_lens,
+                     query_start, parents, q_stride, num_tokens, num_seqs, num_heads, num_kv_heads, head_dim,
+                     block_size, max_blocks_per_seq, scale, num_blocks, dtype, dtype, workspace, workspace_bytes,
+                     stream);
+}
+
+int paged_attention_tree_fp8(void* out, const void* q, const void* k_cache, const void* v_cache,
+                             const float* k_scales, const float* v_scales, const int32_t* block_tables,
+                             const int32_t* context_lens, const int32_t* query_start, const int32_t* parents,
+                             long long q_stride, int num_tokens, int num_seqs, int num_heads, int num_kv_heads,
+                             int head_dim, int block_size, int max_blocks_per_seq, float scale, int num_blocks,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+    if (num_seqs > 0 && num_tokens > 0 && !parents) return PKV_ERR_NULL;
+    return attn_impl(PKV_KERNEL_TREE, out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                     query_start, parents, q_stride, num_tokens, num_seqs, num_heads, num_kv_heads, head_dim,
+                     block_size, max_blocks_per_seq, scale, num_blocks, PKV_BF16, PKV_FP8_E4M3, workspace,
+                     workspace_bytes, stream);
+}
+
+int qk_norm_rope_append(void* q_out, const void* q, const void* k, const void* v, void* k_cache, void* v_cache,
+                        const int64_t* slot_mapping, const int32_t* positions, const float* inv_freq,
+                        const void* q_weight, const void* k_weight, float eps, const int* sections,
+                        int num_sections, int interleaved, long long q_out_stride, long long q_stride,
+                        long long k_stride, long long v_stride, int num_tokens, int num_heads, int num_kv_heads,
+                        int head_dim, int block_size, int num_blocks, int dtype, void* stream) {
+    return rope_impl(q_out, q, k, v, k_cache, v_cache, nullptr, nullptr, slot_mapping, positions, inv_freq, q_weight,
+                     k_weight, eps, sections, num_sections, interleaved, q_out_stride, q_stride, k_stride, v_stride,
+                     num_tokens, num_heads, num_kv_heads, head_dim, block_size, num_blocks, dtype, false, stream);
+}
+
+int qk_norm_rope_append_fp8(void* q_out, const void* q, const void* k, const void* v, void* k_cache, void* v_cache,
+                            const float* k_scales, const float* v_scales, const int64_t* slot_mapping,
+                            const int32_t* positions, const float* inv_freq, const void* q_weight,
+                            const void* k_weight, float eps, const int* sections, int num_sections, int interleaved,
+                            long long q_out_stride, long long q_stride, long long k_stride, long long v_stride,
+                            int num_tokens, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                            int num_blocks, void* stream) {
+    if (num_tokens > 0 && (!k_scales || !v_scales)) return PKV_ERR_NULL;
+    return rope_impl(q_out, q, k, v, k_cache, v_cache, k_scales, v_scales, slot_mapping, positions, inv_freq,
+                     q_weight, k_weight, eps, sections, num_sections, interleaved, q_out_stride, q_stride, k_stride,
+                     v_stride, num_tokens, num_heads, num_kv_heads, head_dim, block_size, num_blocks, PKV_BF16, true,
+                     stream);
 }
 
 int copy_blocks(void* k_cache, void* v_cache, const int64_t* src_dst_pairs, int num_pairs,

@@ -1,0 +1,382 @@
+// attn_common.cuh -- what the multi-query attention kernels share (prompt
+// attention and drafted-tree attention over the paged cache): the launch
+// parameters, the division of the work among CTAs, the rule that says which
+// keys a row sees, and the merge of split items.
+//
+// Rows.  The queries of a sequence that read one kv head are stacked
+// token-major, head-minor: row r of a tile is token r / G of the tile and
+// query head g * G + r % G.  One tile then holds ROWS / G consecutive tokens
+// for all G query heads, every K and V row loaded serves G heads, and a
+// causal tile of the scores is as narrow as the tokens it holds.
+//
+// Work.  An item is (query tile, kv head): its cost is the keys it has to
+// visit plus a constant for its start and end.  Lengths are known on the
+// device only, and a planning launch would cost small calls more than their
+// work does, so every CTA sums the sequences' costs itself (closed forms,
+// one block scan) and takes the b-th of gridDim.x equal intervals of the
+// whole, walking sequence, tile, kv head.  An item that an interval's end
+// cuts is split there; the parts' results are merged by the part that comes
+// last.  Every CTA then has the same work up to one cut's rounding, a CTA
+// leaves at most two partial results, and the cuts, hence the order of every
+// sum, depend on the lengths alone.
+#pragma once
+
+#include <math.h>
+
+#include "common.cuh"
+
+namespace pkv {
+
+struct AttnParams {
+    void* out;
+    const void* q;
+    const void* k_cache;
+    const void* v_cache;
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    const int32_t* query_start;
+    const int32_t* parents;  // tree attention: parent of each draft in its sequence, or -1; else null
+    const float* k_scales;   // fp8 caches, else null
+    const float* v_scales;
+    int* counters;           // [gridDim.x] parts finished of the item whose first part the CTA owns; zero between launches
+    float2* ws_ml;           // [2 gridDim.x][part_rows] (maximum in log2 units, sum)
+    float* ws_o;             // [2 gridDim.x][part_rows][D]
+    int* err;
+    long long q_stride;      // elements between two tokens of q
+    int num_seqs;
+    int num_tokens;
+    int num_heads;
+    int num_kv_heads;
+    int group_log2;          // log2(num_heads / num_kv_heads)
+    int block_size;
+    int max_blocks_per_seq;
+    int num_blocks;
+    int part_rows;           // rows of the largest tile of the call
+    float qscale;            // scale * log2(e)
+    unsigned long long wait_ns;
+};
+
+// ------------------------------------------------------------ the division
+// ROWS: rows of a tile.  A call whose share per CTA is at least COARSE keys
+// cuts items at multiples of FINE keys (balance); a smaller call cuts them at
+// multiples of COARSE only (a part shorter than that costs more in its merge
+// than it saves).  ITEM: cost of an item besides its keys, in keys.
+template <int ROWS_, int FINE_, int COARSE_, int ITEM_>
+struct AttnDivision {
+    static constexpr int ROWS = ROWS_, FINE = FINE_, COARSE = COARSE_, ITEM = ITEM_;
+    static_assert(COARSE % FINE == 0 && (FINE & (FINE - 1)) == 0 && (COARSE & (COARSE - 1)) == 0, "");
+};
+
+// Sequence s of a launch: its rows, and what its tiles cost.
+struct AttnSeq {
+    int q0, n, first;  // first row, queries, position of the first query
+    bool valid;        // false: no valid context; its rows are written as zeros
+
+    __device__ __forceinline__ void load(const AttnParams& p, int s, bool report) {
+        q0 = p.query_start[s];
+        const int q1 = p.query_start[s + 1], ctx = p.context_lens[s];
+        const bool rows_ok = q0 >= 0 && q1 >= q0 && q1 <= p.num_tokens;
+        n = rows_ok ? q1 - q0 : 0;
+        valid = rows_ok && ctx >= n && ctx <= (long long)p.max_blocks_per_seq * p.block_size;
+        first = valid ? ctx - n : 0;
+        if (report && !valid) set_error(p.err, PKV_ERR_DEVICE_BOUNDS);
+    }
+    __device__ __forceinline__ int tiles(int tt) const { return (n + tt - 1) / tt; }
+    // keys tile t visits: those up to its last query's own position
+    __device__ __forceinline__ int keys(int t, int tt) const {
+        if (!valid) return 0;
+        const long long end = (long long)(t + 1) * tt;
+        return first + (end < n ? (int)end : n);
+    }
+    // cost of the tiles before tile t, for one kv head
+    __device__ __forceinline__ long long before(int t, int tt, int item) const {
+        if (!valid) return (long long)t * item;
+        long long c = (long long)t * (first + item) + (long long)tt * t * (t + 1) / 2;
+        if ((long long)t * tt > n) c -= (long long)t * tt - n;  // t past the last tile
+        return c;
+    }
+};
+
+struct AttnItem {
+    int seq;
+    int row;       // row of q / out of the tile's first token
+    int ntok;      // tokens in the tile
+    int pos;       // absolute position of the tile's first token
+    int first;     // position of the sequence's first query (tree: the committed tokens)
+    int kv0, kv1;  // keys of this part
+    int g;         // kv head
+    int part, nparts;
+    int keys;      // keys of the whole item
+    long long at;  // start of the item in the launch's work
+};
+
+template <class Div>
+struct AttnWalk {
+    long long begin, end, at, share;
+    int tt, s, t, g;
+    AttnSeq q;
+
+    // offset (in keys) at which a boundary `o` past the item's start cuts an item of K keys
+    __device__ __forceinline__ static int cut(long long o, int K, long long share) {
+        if (o <= 0) return 0;
+        if (o >= K) return K;
+        if (share >= Div::COARSE) return (int)o & ~(Div::FINE - 1);
+        const int most = K > Div::COARSE ? K - Div::COARSE : 0;  // no part shorter than COARSE
+        return (o < most ? (int)o : most) & ~(Div::COARSE - 1);
+    }
+    // CTA that owns part i of the item (at, K).  With a share of at least
+    // COARSE, a multiple of FINE, the cuts after the first are `share` apart;
+    // with a smaller one every multiple of COARSE up to K - COARSE is cut, and
+    // a part belongs to the last CTA that starts before the part's end.
+    __device__ __forceinline__ static int owner(long long at, int K, long long share, int i) {
+        if (share >= Div::COARSE) {
+            const int b0 = (int)(at / share);
+            const long long o1 = (b0 + 1) * share - at;
+            return b0 + i + (o1 < Div::FINE && o1 < K ? 1 : 0);
+        }
+        const int e = i + 1 < parts(at, K, share) ? (i + 1) * Div::COARSE : K;
+        return (int)((at + e - 1) / share);
+    }
+    __device__ __forceinline__ static int parts(long long at, int K, long long share) {
+        if (share >= Div::COARSE) {
+            const long long o1 = (at / share + 1) * share - at;
+            if (o1 >= K) return 1;
+            return (o1 >= Div::FINE ? 2 : 1) + (int)((K - 1 - o1) / share);
+        }
+        return K < Div::COARSE ? 1 : K / Div::COARSE;
+    }
+
+    // The next item with work for this CTA.
+    __device__ bool next(const AttnParams& p, AttnItem& it) {
+        while (at < end) {
+            const int K = q.keys(t, tt);
+            const long long c = K + Div::ITEM, a = begin - at;
+            const int k0 = cut(a, K, share);
+            const int k1 = at + c <= end ? K : cut(end - at, K, share);
+            const bool mine = K == 0 ? a <= 0 : k0 < k1;
+            if (mine) {
+                it.seq = s;
+                it.row = q.q0 + t * tt;
+                it.ntok = q.n - t * tt < tt ? q.n - t * tt : tt;
+                it.first = q.first;
+                it.pos = q.first + t * tt;
+                it.kv0 = k0;
+                it.kv1 = k1;
+                it.g = g;
+                it.keys = K;
+                it.at = at;
+                it.nparts = 1;
+                it.part = 0;
+                if (k0 > 0 || k1 < K) {
+                    it.nparts = parts(at, K, share);
+                    const int b0 = owner(at, K, share, 0);
+                    // in the first regime the parts' owners follow one another
+                    it.part = share >= Div::COARSE ? (int)blockIdx.x - b0 : k0 / Div::COARSE;
+                }
+            }
+            at += c;
+            if (++g == p.num_kv_heads) {
+                g = 0;
+                if (++t >= q.tiles(tt)) {
+                    t = 0;
+                    while (++s < p.num_seqs) {
+                        q.load(p, s, false);
+                        if (q.n > 0) break;
+                    }
+                    if (s >= p.num_seqs) at = end;
+                }
+            }
+            if (mine) return true;
+        }
+        return false;
+    }
+};
+
+// All NT threads of a CTA: sum the costs and place the walk at the CTA's
+// share.  `scratch` holds NT / 32 + 8 long longs of shared memory; the walk
+// that the threads get is the same for all.  Ends with a barrier.
+template <class Div, int NT>
+__device__ __forceinline__ AttnWalk<Div> attn_walk_start(const AttnParams& p, long long* scratch) {
+    constexpr int NW = NT / 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    AttnWalk<Div> w;
+    w.tt = Div::ROWS >> p.group_log2;
+    const int each = (p.num_seqs + NT - 1) / NT;
+    const int s0 = tid * each < p.num_seqs ? tid * each : p.num_seqs;
+    const int s1 = s0 + each < p.num_seqs ? s0 + each : p.num_seqs;
+    long long mine = 0;
+    for (int s = s0; s < s1; ++s) {
+        AttnSeq q;
+        q.load(p, s, blockIdx.x == 0);
+        mine += q.before(q.tiles(w.tt), w.tt, Div::ITEM) * p.num_kv_heads;
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += v;
+    }
+    if (lane == 31) scratch[warp] = incl;
+    if (tid == 0) scratch[NW + 1] = -1;
+    __syncthreads();
+    long long pre = incl - mine, total = 0;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+        if (i < warp) pre += scratch[i];
+        total += scratch[i];
+    }
+    long long share = (total + gridDim.x - 1) / gridDim.x;
+    if (share >= Div::COARSE) share = (share + Div::FINE - 1) / Div::FINE * Div::FINE;
+    if (share < 1) share = 1;
+    w.share = share;
+    w.begin = share * blockIdx.x;
+    w.end = w.begin + share < total ? w.begin + share : total;
+    if (w.begin < total && pre <= w.begin && w.begin < pre + mine) {
+        for (int s = s0; s < s1; ++s) {
+            AttnSeq q;
+            q.load(p, s, false);
+            const int tiles = q.tiles(w.tt);
+            const long long c = q.before(tiles, w.tt, Div::ITEM) * p.num_kv_heads;
+            if (w.begin < pre + c) {
+                const long long o = w.begin - pre;
+                int lo = 0, hi = tiles - 1;  // the last tile that starts at or before o
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (q.before(mid, w.tt, Div::ITEM) * p.num_kv_heads <= o) lo = mid; else hi = mid - 1;
+                }
+                const long long start = q.before(lo, w.tt, Div::ITEM) * p.num_kv_heads;
+                const int g = (int)((o - start) / (q.keys(lo, w.tt) + Div::ITEM));
+                scratch[NW + 1] = s;
+                scratch[NW + 2] = lo;
+                scratch[NW + 3] = g;
+                scratch[NW + 4] = pre + start + (long long)g * (q.keys(lo, w.tt) + Div::ITEM);
+                break;
+            }
+            pre += c;
+        }
+    }
+    __syncthreads();
+    w.s = (int)scratch[NW + 1];
+    if (w.s < 0) {
+        w.at = w.end = w.begin;  // nothing to do
+        w.s = w.t = w.g = 0;
+        return w;
+    }
+    w.t = (int)scratch[NW + 2];
+    w.g = (int)scratch[NW + 3];
+    w.at = scratch[NW + 4];
+    w.q.load(p, w.s, false);
+    return w;
+}
+
+// ------------------------------------------------------------------- masks
+// Whether the query at index `i` of its sequence (position first + i) sees
+// key position `key`: the keys up to its own position, or, with a tree, the
+// committed tokens (key < first), itself and its ancestors.  The walk goes
+// from parent to parent while the index stays above the key's; a parent that
+// is not smaller than its child ends it (and is reported, attn_check_parents).
+__device__ __forceinline__ bool sees(const int32_t* parents_of_seq, int first, int i, int key) {
+    if (parents_of_seq == nullptr) return key <= first + i;
+    const int d = key - first;
+    if (d < 0) return true;
+    while (i > d) {
+        const int up = parents_of_seq[i];
+        if (up >= i) return false;
+        i = up;
+    }
+    return i == d;
+}
+
+// A draft's parent is -1 or comes before it in its sequence.
+__device__ __forceinline__ void attn_check_parents(const AttnParams& p, const AttnItem& it, int tid, int nt) {
+    for (int i = tid; i < it.ntok; i += nt) {
+        const int up = p.parents[it.row + i];
+        if (up < -1 || up >= it.pos - it.first + i) set_error(p.err, PKV_ERR_DEVICE_BOUNDS);
+    }
+}
+
+// ------------------------------------------------------------------- merge
+// First partial row of part i of an item that CTA b owns: a CTA's first item
+// may go on from the CTA before (part > 0), its last may go on in the next.
+__device__ __forceinline__ long long attn_partial_row(const AttnParams& p, int b, int part) {
+    return (long long)(2 * b + (part == 0 ? 1 : 0)) * p.part_rows;
+}
+
+// End of one part of a split item, called by NT threads (tid, sync() a
+// barrier over them) once they have written the part's rows to ws_o / ws_ml.
+// The last part to arrive merges all of them in their order,
+//     M = max m_i,  out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,
+// so the result does not depend on which part came last, and zeroes the
+// counter for the next launch.  A warp takes one row at a time.
+template <class Div, typename T, int D, int NT, class Sync>
+__device__ __forceinline__ void attn_merge(const AttnParams& p, const AttnItem& it, long long share, int* flag,
+                                           int tid, Sync&& sync) {
+    using Walk = AttnWalk<Div>;
+    const int G = 1 << p.group_log2;
+    const int rows = it.ntok << p.group_log2;
+    __threadfence();
+    sync();
+    if (tid == 0) {
+        int* count = p.counters + Walk::owner(it.at, it.keys, share, 0);
+        const int last = atomicAdd(count, 1) == it.nparts - 1;
+        if (last) *count = 0;
+        *flag = last;
+    }
+    sync();
+    if (!*flag) return;
+    __threadfence();
+    const int warp = tid >> 5, lane = tid & 31;
+    constexpr int VE = D / 32;  // values of a row per lane
+    for (int r = warp; r < rows; r += NT / 32) {
+        float M = -INFINITY, L = 0.f, acc[VE];
+#pragma unroll
+        for (int e = 0; e < VE; ++e) acc[e] = 0.f;
+        for (int i0 = 0; i0 < it.nparts; i0 += 32) {
+            // a lane looks up one part's maximum and sum
+            const int i = i0 + lane;
+            long long pr = 0;
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if (i < it.nparts) {
+                pr = attn_partial_row(p, Walk::owner(it.at, it.keys, share, i), i) + r;
+                ml = __ldcg(&p.ws_ml[pr]);
+            }
+            float mx = ml.x;
+#pragma unroll
+            for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            const float Mn = fmaxf(M, mx);
+            const float alpha = Mn == -INFINITY ? 1.f : exp2f(M - Mn);
+            M = Mn;
+            L *= alpha;
+#pragma unroll
+            for (int e = 0; e < VE; ++e) acc[e] *= alpha;
+            // no key seen in any part: all sums are 0 (or NaN), taken as they are
+            const float w = Mn == -INFINITY ? 1.f : exp2f(ml.x - Mn);
+            const int count = it.nparts - i0 < 32 ? it.nparts - i0 : 32;
+#pragma unroll 4
+            for (int j = 0; j < count; ++j) {
+                const float wj = __shfl_sync(0xffffffffu, w, j);
+                const long long prj = __shfl_sync(0xffffffffu, pr, j);
+                L = fmaf(wj, __shfl_sync(0xffffffffu, ml.y, j), L);
+                const float* o = p.ws_o + prj * D + lane * VE;
+                if constexpr (VE == 4) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4*>(o));
+                    acc[0] = fmaf(wj, v.x, acc[0]);
+                    acc[1] = fmaf(wj, v.y, acc[1]);
+                    acc[2] = fmaf(wj, v.z, acc[2]);
+                    acc[3] = fmaf(wj, v.w, acc[3]);
+                } else {
+                    const float2 v = __ldcg(reinterpret_cast<const float2*>(o));
+                    acc[0] = fmaf(wj, v.x, acc[0]);
+                    acc[1] = fmaf(wj, v.y, acc[1]);
+                }
+            }
+        }
+        const float inv = L == 0.f ? 0.f : 1.f / L;  // no key seen: a zero row
+        T* dst = static_cast<T*>(p.out) +
+                 ((long long)(it.row + (r >> p.group_log2)) * p.num_heads + it.g * G + (r & (G - 1))) * D + lane * VE;
+#pragma unroll
+        for (int e = 0; e < VE; ++e) Elem<T>::store(dst + e, acc[e] * inv);
+    }
+}
+
+}  // namespace pkv

@@ -1,0 +1,56 @@
+// attn_simt.cu -- launch of the CUDA-core multi-query attention.
+#include <atomic>
+
+#include "attn_launch.h"
+#include "attn_simt.cuh"
+
+namespace pkv {
+namespace {
+
+template <typename T, typename TKV, int D>
+cudaError_t launch_inst(const AttnParams& p, cudaStream_t st) {
+    using C = SimtCfg<D>;
+    auto kern = attn_simt_kernel<T, TKV, D>;
+    static std::atomic<unsigned long long> configured{0};  // one bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(configured.load() & bit)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+        if (e != cudaSuccess) return e;
+        configured.fetch_or(bit);
+    }
+    // a programmatic dependent of the append or rotation before it
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(kAttnSms * C::CTAS_PER_SM));
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM_BYTES;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <typename T, typename TKV>
+cudaError_t launch_dim(const AttnParams& p, int D, cudaStream_t st) {
+    return D == 64 ? launch_inst<T, TKV, 64>(p, st) : launch_inst<T, TKV, 128>(p, st);
+}
+
+}  // namespace
+
+AttnShape attn_shape(int kv_dtype) {
+    (void)kv_dtype;
+    return AttnShape{kAttnSms * SimtCfg<64>::CTAS_PER_SM, SimtCfg<64>::ROWS};
+}
+
+cudaError_t launch_attn(const AttnParams& p, int dtype, int kv_dtype, int D, cudaStream_t st) {
+    if (kv_dtype == PKV_FP8_E4M3) return launch_dim<__nv_bfloat16, __nv_fp8_e4m3>(p, D, st);
+    if (dtype == PKV_BF16) return launch_dim<__nv_bfloat16, __nv_bfloat16>(p, D, st);
+    return launch_dim<float, float>(p, D, st);
+}
+
+}  // namespace pkv

@@ -43,10 +43,15 @@ KERNEL_DECODE = 0
 KERNEL_APPEND = 1
 KERNEL_COPY_BLOCKS = 2
 KERNEL_SWAP_BLOCKS = 3
+KERNEL_PREFILL = 4
+KERNEL_TREE = 5
+KERNEL_QK_ROPE = 6
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
+_F = ctypes.c_float
+_LL = ctypes.c_longlong
 
 # name -> (restype, argtypes); the order mirrors include/pagedkv.h
 SIGNATURES = {
@@ -61,6 +66,13 @@ SIGNATURES = {
     "paged_attention_decode_noalloc": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I,
                                             ctypes.c_float, _I, _I, _I, _P]),
     "kv_cache_append": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
+    "qk_norm_rope_append": (_I, [_P] * 11 + [_F, _P, _I, _I] + [_LL] * 4 + [_I] * 7 + [_P]),
+    "qk_norm_rope_append_fp8": (_I, [_P] * 13 + [_F, _P, _I, _I] + [_LL] * 4 + [_I] * 6 + [_P]),
+    "paged_attention_prefill": (_I, [_P] * 7 + [_LL] + [_I] * 7 + [_F, _I, _I, _P, _SZ, _P]),
+    "paged_attention_prefill_fp8": (_I, [_P] * 9 + [_LL] + [_I] * 7 + [_F, _I, _P, _SZ, _P]),
+    "paged_attention_tree": (_I, [_P] * 8 + [_LL] + [_I] * 7 + [_F, _I, _I, _P, _SZ, _P]),
+    "paged_attention_tree_fp8": (_I, [_P] * 10 + [_LL] + [_I] * 7 + [_F, _I, _P, _SZ, _P]),
+    "paged_attention_prefill_workspace_size": (_SZ, [_I] * 5),
     "copy_blocks": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
     "swap_blocks": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P]),
     "pkv_bm_create": (_P, [_I, _I, _I, _P]),
@@ -169,6 +181,7 @@ def _dev(t: torch.Tensor, name: str, dtype=None, *, device=None, shape=None) -> 
 # sharing the buffer between them is safe; different streams get different
 # buffers.
 _workspaces: dict = {}
+_prefill_workspaces: dict = {}  # the same for prompt and drafted-tree attention
 
 
 def _torch_stream(stream_handle: int, dev: torch.device):
@@ -177,13 +190,13 @@ def _torch_stream(stream_handle: int, dev: torch.device):
     return torch.cuda.ExternalStream(stream_handle, device=dev)
 
 
-def _workspace_for(need: int, dev: torch.device, stream_handle: int) -> torch.Tensor:
+def _workspace_for(need: int, dev: torch.device, stream_handle: int, kept: dict = _workspaces) -> torch.Tensor:
     key = (dev.index, stream_handle)
-    ws = _workspaces.get(key)
+    ws = kept.get(key)
     if ws is None or ws.numel() < need:
         with torch.cuda.stream(_torch_stream(stream_handle, dev)):
             ws = torch.zeros(need + need // 4, dtype=torch.uint8, device=dev)
-        _workspaces[key] = ws
+        kept[key] = ws
     return ws
 
 
@@ -365,6 +378,171 @@ def kv_cache_append(k_cache, v_cache, k, v, slot_mapping, stream=None) -> None:
     with torch.cuda.device(dev):
         rc = lib.kv_cache_append(*args, T, Hkv, D, bs, N, _dtype_code(k_cache), _stream(stream, dev))
     _check(rc, "kv_cache_append")
+
+
+def _rows(t: torch.Tensor, name: str, dtype, device, shape) -> tuple[int, int]:
+    """(device pointer, elements between two tokens) of [tokens][heads][head_dim]
+    rows: the heads of a token are contiguous, tokens may lie apart (a slice
+    of a projection's output)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    T, H, D = shape
+    if t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if T > 1 and t.stride(0) < H * D:
+        raise ValueError(f"{name}: tokens must not overlap")
+    return t.data_ptr(), t.stride(0) if T > 1 else H * D
+
+
+def qk_norm_rope_append(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, inv_freq, *, q_weight=None,
+                        k_weight=None, eps: float = 1e-6, sections=None, interleaved: bool = False,
+                        stream=None) -> None:
+    """Per-head RMS norm of q [T][H][D] and k [T][Hkv][D] (where a weight [D]
+    is given), position rotation of both, q into q_out, k and v into the
+    caches at slot_mapping (int64 [T]; negative: none).  ``positions`` int32
+    [T], or [axes][T] with ``sections``, the number of frequencies of each
+    axis; ``inv_freq`` float32, one value per rotated pair.  q, k, v and q_out
+    may be slices over heads of one tensor; q_out may be q."""
+    _rope("qk_norm_rope_append", q_out, q, k, v, k_cache, v_cache, None, slot_mapping, positions, inv_freq,
+          q_weight, k_weight, eps, sections, interleaved, stream)
+
+
+def qk_norm_rope_append_fp8(q_out, q, k, v, k_cache, v_cache, k_scales, v_scales, slot_mapping, positions,
+                            inv_freq, *, q_weight=None, k_weight=None, eps: float = 1e-6, sections=None,
+                            interleaved: bool = False, stream=None) -> None:
+    """The same into fp8 pools with per-kv-head float32 scales; q, k, v bf16."""
+    _rope("qk_norm_rope_append_fp8", q_out, q, k, v, k_cache, v_cache, (k_scales, v_scales), slot_mapping,
+          positions, inv_freq, q_weight, k_weight, eps, sections, interleaved, stream)
+
+
+def _rope(name, q_out, q, k, v, k_cache, v_cache, scales, slot_mapping, positions, inv_freq, q_weight, k_weight,
+          eps, sections, interleaved, stream):
+    T, H, D = q.shape
+    N, Hkv, bs, D2 = k_cache.shape
+    if D2 != D or tuple(v_cache.shape) != tuple(k_cache.shape):
+        raise ValueError("shape mismatch between q and the caches")
+    pairs = inv_freq.shape[0]
+    sections = [pairs] if sections is None else [int(x) for x in sections]
+    if sum(sections) != pairs:
+        raise ValueError(f"sections {sections} do not add up to the {pairs} frequencies")
+    if T == 0:
+        return
+    dev = _device(q)
+    act = torch.bfloat16 if scales is not None else k_cache.dtype
+    pool = torch.float8_e4m3fn if scales is not None else act
+    want = (T,) if positions.dim() == 1 and len(sections) == 1 else (len(sections), T)
+    rows = [_rows(q_out, "q_out", act, dev, (T, H, D)), _rows(q, "q", act, dev, (T, H, D)),
+            _rows(k, "k", act, dev, (T, Hkv, D)), _rows(v, "v", act, dev, (T, Hkv, D))]
+    args = [r[0] for r in rows]
+    args += [_dev(k_cache, "k_cache", pool, device=dev), _dev(v_cache, "v_cache", pool, device=dev)]
+    if scales is not None:
+        args += [_dev(s, n, torch.float32, device=dev, shape=(Hkv,))
+                 for s, n in zip(scales, ("k_scales", "v_scales"))]
+    args += [_dev(slot_mapping, "slot_mapping", torch.int64, device=dev, shape=(T,)),
+             _dev(positions, "positions", torch.int32, device=dev, shape=want),
+             _dev(inv_freq, "inv_freq", torch.float32, device=dev, shape=(pairs,))]
+    args += [None if w is None else _dev(w, n, act, device=dev, shape=(D,))
+             for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight"))]
+    args += [float(eps), (ctypes.c_int * len(sections))(*sections), len(sections), int(bool(interleaved))]
+    args += [r[1] for r in rows] + [T, H, Hkv, D, bs, N]
+    if scales is None:
+        args.append(_dtype_code(q))
+    with torch.cuda.device(dev):
+        rc = getattr(lib, name)(*args, _stream(stream, dev))
+    _check(rc, name)
+
+
+def paged_attention_prefill_workspace_size(num_tokens: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                                           cache_dtype: int = PKV_BF16) -> int:
+    return int(lib.paged_attention_prefill_workspace_size(num_tokens, num_heads, num_kv_heads, head_dim,
+                                                          cache_dtype))
+
+
+def paged_attention_prefill(out, q, k_cache, v_cache, block_tables, context_lens, query_start, scale: float, *,
+                            num_blocks: int | None = None, workspace: torch.Tensor | None = None,
+                            stream=None) -> None:
+    """Causal attention of packed prompts, or chunks of them, whose K and V are
+    in the cache: out, q [T][H][D] (q may be a slice over heads);
+    query_start int32 [B + 1]; context_lens int32 [B] count the new tokens
+    too.  Rows from query_start[B] on are left as they are.  ``workspace``: a
+    zero-initialised uint8 CUDA tensor of at least
+    :func:`paged_attention_prefill_workspace_size` bytes, or None for a buffer
+    this module keeps per (device, stream): a call that is captured into a
+    graph needs its own."""
+    _attend("paged_attention_prefill", out, q, k_cache, v_cache, None, block_tables, context_lens, query_start,
+            None, scale, num_blocks, workspace, stream)
+
+
+def paged_attention_prefill_fp8(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                                query_start, scale: float, *, num_blocks: int | None = None,
+                                workspace: torch.Tensor | None = None, stream=None) -> None:
+    """The same over fp8 caches with per-kv-head float32 scales; q and out bf16."""
+    _attend("paged_attention_prefill_fp8", out, q, k_cache, v_cache, (k_scales, v_scales), block_tables,
+            context_lens, query_start, None, scale, num_blocks, workspace, stream)
+
+
+def paged_attention_tree(out, q, k_cache, v_cache, block_tables, context_lens, query_start, parents,
+                         scale: float, *, num_blocks: int | None = None, workspace: torch.Tensor | None = None,
+                         stream=None) -> None:
+    """Attention of trees of drafted tokens: as :func:`paged_attention_prefill`,
+    but query i of a sequence attends the committed tokens (its context
+    without the queries), itself and its ancestors.  parents int32 [T]: index
+    of the parent among the sequence's drafts, below the draft's own, or -1."""
+    _attend("paged_attention_tree", out, q, k_cache, v_cache, None, block_tables, context_lens, query_start,
+            parents, scale, num_blocks, workspace, stream)
+
+
+def paged_attention_tree_fp8(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                             query_start, parents, scale: float, *, num_blocks: int | None = None,
+                             workspace: torch.Tensor | None = None, stream=None) -> None:
+    """The same over fp8 caches with per-kv-head float32 scales; q and out bf16."""
+    _attend("paged_attention_tree_fp8", out, q, k_cache, v_cache, (k_scales, v_scales), block_tables,
+            context_lens, query_start, parents, scale, num_blocks, workspace, stream)
+
+
+def _attend(name, out, q, k_cache, v_cache, scales, block_tables, context_lens, query_start, parents, scale,
+            num_blocks, workspace, stream):
+    T, H, D = q.shape
+    N, Hkv, bs, D2 = k_cache.shape
+    if D2 != D or tuple(out.shape) != (T, H, D) or tuple(v_cache.shape) != tuple(k_cache.shape):
+        raise ValueError("shape mismatch between q, out and the caches")
+    B = context_lens.shape[0]
+    maxb = _tables(block_tables, context_lens, B)
+    dev = _device(q)
+    act = torch.bfloat16 if scales is not None else k_cache.dtype
+    pool = torch.float8_e4m3fn if scales is not None else act
+    q_ptr, q_stride = _rows(q, "q", act, dev, (T, H, D))
+    args = [_dev(out, "out", act, device=dev), q_ptr, _dev(k_cache, "k_cache", pool, device=dev),
+            _dev(v_cache, "v_cache", pool, device=dev)]
+    if scales is not None:
+        args += [_dev(s, n, torch.float32, device=dev, shape=(Hkv,))
+                 for s, n in zip(scales, ("k_scales", "v_scales"))]
+    args += [_dev(block_tables, "block_tables", torch.int32, device=dev),
+             _dev(context_lens, "context_lens", torch.int32, device=dev),
+             _dev(query_start, "query_start", torch.int32, device=dev, shape=(B + 1,))]
+    if name.startswith("paged_attention_tree"):
+        args.append(_dev(parents, "parents", torch.int32, device=dev, shape=(T,)))
+    need = paged_attention_prefill_workspace_size(T, H, Hkv, D, _dtype_code(k_cache))
+    st = _stream(stream, dev)
+    if workspace is None and need > 0:
+        with torch.cuda.stream(_torch_stream(st, dev)):
+            if torch.cuda.is_current_stream_capturing():
+                raise ValueError(f"{name}: pass a workspace to a call that is captured into a graph")
+        workspace = _workspace_for(need, dev, st, _prefill_workspaces)
+    ws_ptr = _dev(workspace, "workspace", torch.uint8, device=dev) if workspace is not None else None
+    ws_bytes = workspace.numel() if workspace is not None else 0
+    args += [q_stride, T, B, H, Hkv, D, bs, maxb, float(scale), N if num_blocks is None else int(num_blocks)]
+    if scales is None:
+        args.append(_dtype_code(q))
+    with torch.cuda.device(dev):
+        rc = getattr(lib, name)(*args, ws_ptr, ws_bytes, st)
+    _check(rc, name)
 
 
 def copy_blocks(k_cache, v_cache, src_dst_pairs, stream=None) -> None:
