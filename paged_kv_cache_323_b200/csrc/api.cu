@@ -437,7 +437,9 @@ int decode_impl(void* out, const void* q, const void* k_cache, const void* v_cac
 namespace {
 
 // Workspace of the multi-query attention: one counter per CTA of the grid
-// (zero between launches), then the partial results, two per CTA.
+// (zero between launches), in a region of its own whatever kernel the call
+// runs on, then the partial results, two per CTA.
+constexpr int kAttnCounters = 512;
 struct AttnLayout {
     pkv::AttnShape shape;
     int part_rows;
@@ -446,10 +448,10 @@ struct AttnLayout {
 
 AttnLayout attn_layout(long long num_tokens, long long group, long long D, int kv_dtype) {
     AttnLayout w;
-    w.shape = pkv::attn_shape(kv_dtype);
+    w.shape = kv_dtype == PKV_F32 ? pkv::attn_simt_shape() : pkv::attn_tc_shape();
     w.part_rows = num_tokens * group < w.shape.rows ? (int)(num_tokens * group) : w.shape.rows;
     const size_t rows = size_t(2) * w.shape.grid * w.part_rows;
-    w.ml_off = align256(w.shape.grid * sizeof(int));
+    w.ml_off = kAttnCounters * sizeof(int);
     w.o_off = w.ml_off + align256(rows * sizeof(float2));
     w.total = w.o_off + align256(rows * D * sizeof(float));
     return w;
@@ -475,6 +477,7 @@ int attn_impl(int kind, void* out, const void* q, const void* k_cache, const voi
     if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache)) return PKV_ERR_INVALID;
     if (q_stride < (long long)num_heads * head_dim || q_stride * elt_bytes(dtype) % 16 != 0) return PKV_ERR_INVALID;
     if ((long long)max_blocks_per_seq * block_size > INT_MAX - 1024) return PKV_ERR_INVALID;
+    if ((long long)num_blocks * num_kv_heads > INT_MAX) return PKV_ERR_INVALID;  // slices have 31-bit indices
     const AttnLayout w = attn_layout(num_tokens, group, head_dim, kv_dtype);
     if (workspace == nullptr || workspace_bytes < w.total || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
         return PKV_ERR_WORKSPACE;
@@ -511,7 +514,9 @@ int attn_impl(int kind, void* out, const void* q, const void* k_cache, const voi
     p.qscale = scale * 1.4426950408889634f;  // log2(e): softmax runs in base 2
     p.wait_ns = g_wait_ns.load();
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return launch(kind, st, [&] { return pkv::launch_attn(p, dtype, kv_dtype, head_dim, st); });
+    return launch(kind, st, [&] {
+        return dtype == PKV_F32 ? pkv::launch_attn_simt(p, head_dim, st) : pkv::launch_attn_tc(p, fp8, head_dim, st);
+    });
 }
 
 int rope_impl(void* q_out, const void* q, const void* k, const void* v, void* k_cache, void* v_cache,

@@ -307,23 +307,25 @@ __device__ __forceinline__ long long attn_partial_row(const AttnParams& p, int b
 // The last part to arrive merges all of them in their order,
 //     M = max m_i,  out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,
 // so the result does not depend on which part came last, and zeroes the
-// counter for the next launch.  A warp takes one row at a time.
+// counter for the next launch.  A warp takes one row at a time.  `turns`
+// counts the parts this CTA has reported.  False when a barrier gave up.
 template <class Div, typename T, int D, int NT, class Sync>
-__device__ __forceinline__ void attn_merge(const AttnParams& p, const AttnItem& it, long long share, int* flag,
-                                           int tid, Sync&& sync) {
+__device__ __forceinline__ bool attn_merge(const AttnParams& p, const AttnItem& it, long long share, int* flag,
+                                           int* turns, int tid, Sync&& sync) {
     using Walk = AttnWalk<Div>;
     const int G = 1 << p.group_log2;
     const int rows = it.ntok << p.group_log2;
     __threadfence();
-    sync();
+    if (!sync()) return false;
     if (tid == 0) {
         int* count = p.counters + Walk::owner(it.at, it.keys, share, 0);
         const int last = atomicAdd(count, 1) == it.nparts - 1;
         if (last) *count = 0;
         *flag = last;
+        *turns += 1;
     }
-    sync();
-    if (!*flag) return;
+    if (!sync()) return false;
+    if (!*flag) return true;
     __threadfence();
     const int warp = tid >> 5, lane = tid & 31;
     constexpr int VE = D / 32;  // values of a row per lane
@@ -377,6 +379,7 @@ __device__ __forceinline__ void attn_merge(const AttnParams& p, const AttnItem& 
 #pragma unroll
         for (int e = 0; e < VE; ++e) Elem<T>::store(dst + e, acc[e] * inv);
     }
+    return true;
 }
 
 }  // namespace pkv

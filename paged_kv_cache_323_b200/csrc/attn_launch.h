@@ -11,16 +11,19 @@ namespace pkv {
 
 constexpr int kAttnSms = 148;
 
+// The workspace holds 512 counters: no grid is larger.
+
 // What a launch asks of its workspace: CTAs of the grid (two partial results
 // each) and rows of a full tile.
 struct AttnShape {
     int grid;
     int rows;
 };
-AttnShape attn_shape(int kv_dtype);
-
-// dtype: q and out; kv_dtype: the caches (dtype, or PKV_FP8_E4M3 with bf16 q).
-cudaError_t launch_attn(const AttnParams& p, int dtype, int kv_dtype, int D, cudaStream_t st);
+// fp32 caches on the CUDA cores; bf16 and fp8 ones (bf16 q) on the tensor cores
+AttnShape attn_simt_shape();
+cudaError_t launch_attn_simt(const AttnParams& p, int D, cudaStream_t st);
+AttnShape attn_tc_shape();
+cudaError_t launch_attn_tc(const AttnParams& p, bool fp8, int D, cudaStream_t st);
 
 cudaError_t launch_qk_rope(const RopeParams& p, int dtype, bool fp8, bool interleaved, int D, cudaStream_t st);
 

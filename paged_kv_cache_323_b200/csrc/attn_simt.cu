@@ -7,10 +7,10 @@
 namespace pkv {
 namespace {
 
-template <typename T, typename TKV, int D>
+template <int D>
 cudaError_t launch_inst(const AttnParams& p, cudaStream_t st) {
     using C = SimtCfg<D>;
-    auto kern = attn_simt_kernel<T, TKV, D>;
+    auto kern = attn_simt_kernel<D>;
     static std::atomic<unsigned long long> configured{0};  // one bit per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -35,22 +35,12 @@ cudaError_t launch_inst(const AttnParams& p, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-template <typename T, typename TKV>
-cudaError_t launch_dim(const AttnParams& p, int D, cudaStream_t st) {
-    return D == 64 ? launch_inst<T, TKV, 64>(p, st) : launch_inst<T, TKV, 128>(p, st);
-}
-
 }  // namespace
 
-AttnShape attn_shape(int kv_dtype) {
-    (void)kv_dtype;
-    return AttnShape{kAttnSms * SimtCfg<64>::CTAS_PER_SM, SimtCfg<64>::ROWS};
-}
+AttnShape attn_simt_shape() { return AttnShape{kAttnSms * SimtCfg<64>::CTAS_PER_SM, SimtDivision::ROWS}; }
 
-cudaError_t launch_attn(const AttnParams& p, int dtype, int kv_dtype, int D, cudaStream_t st) {
-    if (kv_dtype == PKV_FP8_E4M3) return launch_dim<__nv_bfloat16, __nv_fp8_e4m3>(p, D, st);
-    if (dtype == PKV_BF16) return launch_dim<__nv_bfloat16, __nv_bfloat16>(p, D, st);
-    return launch_dim<float, float>(p, D, st);
+cudaError_t launch_attn_simt(const AttnParams& p, int D, cudaStream_t st) {
+    return D == 64 ? launch_inst<64>(p, st) : launch_inst<128>(p, st);
 }
 
 }  // namespace pkv

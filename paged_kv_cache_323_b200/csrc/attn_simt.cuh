@@ -38,20 +38,9 @@ struct SimtCfg {
     static_assert(ROWS * LP <= KEYS * LD, "the probabilities reuse K's space");
 };
 
-// Four consecutive elements as fp32.
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-    const uint2 w = *reinterpret_cast<const uint2*>(p);
-    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                       __uint_as_float(w.y & 0xffff0000u));
-}
-__device__ __forceinline__ float4 load4(const __nv_fp8_e4m3* p) {
-    float f[16];
-    Elem<__nv_fp8_e4m3>::unpack(make_uint4(*reinterpret_cast<const uint32_t*>(p), 0u, 0u, 0u), f);
-    return make_float4(f[0], f[1], f[2], f[3]);
-}
 
-template <typename T, typename TKV, int D>
+template <int D>
 __global__ void __launch_bounds__(256, 2) attn_simt_kernel(const AttnParams p) {
     using C = SimtCfg<D>;
     extern __shared__ __align__(16) float simt_smem[];
@@ -59,7 +48,7 @@ __global__ void __launch_bounds__(256, 2) attn_simt_kernel(const AttnParams p) {
     float* sk = simt_smem + C::K_OFF;
     float* sp = sk;
     float* sv = simt_smem + C::V_OFF;
-    __shared__ int flag;
+    __shared__ int flag, turns;
     __shared__ AttnItem item[2];
     __shared__ long long walk_scratch[C::THREADS / 32 + 8];
     const int tid = threadIdx.x;
@@ -78,8 +67,7 @@ __global__ void __launch_bounds__(256, 2) attn_simt_kernel(const AttnParams p) {
         if (u.seq < 0) break;
         const int g = u.g;
         const int rows = u.ntok << p.group_log2;
-        const float qscale = p.k_scales ? p.qscale * p.k_scales[g] : p.qscale;
-        const float vscale = p.v_scales ? p.v_scales[g] : 1.f;
+        const float qscale = p.qscale;
         const int32_t* bt = p.block_tables + (long long)u.seq * p.max_blocks_per_seq;
         const int32_t* par = p.parents ? p.parents + (u.row - (u.pos - u.first)) : nullptr;
         if (par != nullptr && u.part == 0 && g == 0) attn_check_parents(p, u, tid, C::THREADS);
@@ -87,7 +75,7 @@ __global__ void __launch_bounds__(256, 2) attn_simt_kernel(const AttnParams p) {
             const int r = i / C4, c = i % C4;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < rows)
-                v = load4(static_cast<const T*>(p.q) + (long long)(u.row + (r >> p.group_log2)) * p.q_stride +
+                v = load4(static_cast<const float*>(p.q) + (long long)(u.row + (r >> p.group_log2)) * p.q_stride +
                           (g * G + (r & (G - 1))) * D + 4 * c);
             *reinterpret_cast<float4*>(sq + r * C::LD + c * 4) = v;
         }
@@ -114,8 +102,8 @@ __global__ void __launch_bounds__(256, 2) attn_simt_kernel(const AttnParams p) {
                         bad = 1;
                     } else {
                         const long long at = (((long long)e * Hkv + g) * bs + key % bs) * D;
-                        kv = load4(static_cast<const TKV*>(p.k_cache) + at + 4 * c);
-                        vv = load4(static_cast<const TKV*>(p.v_cache) + at + 4 * c);
+                        kv = load4(static_cast<const float*>(p.k_cache) + at + 4 * c);
+                        vv = load4(static_cast<const float*>(p.v_cache) + at + 4 * c);
                     }
                 }
                 *reinterpret_cast<float4*>(sk + r * C::LD + c * 4) = kv;
@@ -224,25 +212,28 @@ __global__ void __launch_bounds__(256, 2) attn_simt_kernel(const AttnParams p) {
             const int r = 4 * ty + i;
             if (r >= rows) continue;
             if (u.nparts == 1) {
-                const float inv = l[i] == 0.f ? 0.f : vscale / l[i];  // no key seen: a zero row
-                T* dst = static_cast<T*>(p.out) +
+                const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];  // no key seen: a zero row
+                float* dst = static_cast<float*>(p.out) +
                          ((long long)(u.row + (r >> p.group_log2)) * p.num_heads + g * G + (r & (G - 1))) * D;
 #pragma unroll
                 for (int j = 0; j < OJ; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) Elem<T>::store(dst + 64 * j + 4 * tx + e, o[i][4 * j + e] * inv);
+                    *reinterpret_cast<float4*>(dst + 64 * j + 4 * tx) = make_float4(
+                        o[i][4 * j] * inv, o[i][4 * j + 1] * inv, o[i][4 * j + 2] * inv, o[i][4 * j + 3] * inv);
             } else {
                 const long long pr = attn_partial_row(p, blockIdx.x, u.part) + r;
                 if (tx == 0) p.ws_ml[pr] = make_float2(m[i], l[i]);
 #pragma unroll
                 for (int j = 0; j < OJ; ++j)
                     *reinterpret_cast<float4*>(p.ws_o + pr * D + 64 * j + 4 * tx) =
-                        make_float4(o[i][4 * j] * vscale, o[i][4 * j + 1] * vscale, o[i][4 * j + 2] * vscale,
-                                    o[i][4 * j + 3] * vscale);
+                        make_float4(o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2],
+                                    o[i][4 * j + 3]);
             }
         }
         if (u.nparts > 1)
-            attn_merge<SimtDivision, T, D, C::THREADS>(p, u, walk.share, &flag, tid, [] { __syncthreads(); });
+            attn_merge<SimtDivision, float, D, C::THREADS>(p, u, walk.share, &flag, &turns, tid, [] {
+                __syncthreads();
+                return true;
+            });
     }
 }
 

@@ -221,6 +221,19 @@ def test_same_bits_every_time_and_after_other_shapes(pk, dtype):
         assert torch.equal(big.call(pk, True), first)
 
 
+def test_one_workspace_for_every_kernel(pk):
+    """Split calls over fp32, bf16 and fp8 caches in turn through one workspace."""
+    calls = [Batch([(5, 9000), (64, 3000)], dtype=d, heads=h, kv_heads=1, head_dim=n, seed=25)
+             for d, h, n in (("f32", 8, 128), ("bf16", 4, 128), ("f32", 1, 64), ("fp8", 8, 64))]
+    need = max(pk.paged_attention_prefill_workspace_size(b.T, b.H, b.G, b.D, pk._dtype_code(b.kc)) for b in calls)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    refs = [attend(b) for b in calls]
+    for _ in range(3):
+        for b, (ref, bound) in zip(calls, refs):
+            b.out.fill_(-77.0)
+            close(b.call(pk, workspace=ws), ref, bound, b.dtype)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "fp8"])
 def test_streams_and_graphs(pk, dtype):
     """Two streams at once with workspaces of their own, and a captured call replayed on new data."""
