@@ -307,8 +307,8 @@ __device__ __forceinline__ long long attn_partial_row(const AttnParams& p, int b
 // The last part to arrive merges all of them in their order,
 //     M = max m_i,  out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,
 // so the result does not depend on which part came last, and zeroes the
-// counter for the next launch.  A warp takes one row at a time.  `turns`
-// counts the parts this CTA has reported.  False when a barrier gave up.
+// counter for the next launch.  `turns` counts the parts this CTA has
+// reported.  False when a barrier gave up.
 template <class Div, typename T, int D, int NT, class Sync>
 __device__ __forceinline__ bool attn_merge(const AttnParams& p, const AttnItem& it, long long share, int* flag,
                                            int* turns, int tid, Sync&& sync) {
@@ -327,57 +327,84 @@ __device__ __forceinline__ bool attn_merge(const AttnParams& p, const AttnItem& 
     if (!sync()) return false;
     if (!*flag) return true;
     __threadfence();
+    // A warp has rows warp, warp + NT / 32, ..: lane k looks after the maxima and sums
+    // of the k-th of them, then the warp adds up RB rows x PB parts at a time, so that
+    // many loads are in flight whether the rows are many or the parts.
+    constexpr int NW = NT / 32, VE = D / 32, RB = 4, PB = 4;
+    static_assert(Div::ROWS <= 32 * NW, "a lane per row");
     const int warp = tid >> 5, lane = tid & 31;
-    constexpr int VE = D / 32;  // values of a row per lane
-    for (int r = warp; r < rows; r += NT / 32) {
-        float M = -INFINITY, L = 0.f, acc[VE];
-#pragma unroll
-        for (int e = 0; e < VE; ++e) acc[e] = 0.f;
-        for (int i0 = 0; i0 < it.nparts; i0 += 32) {
-            // a lane looks up one part's maximum and sum
-            const int i = i0 + lane;
-            long long pr = 0;
-            float2 ml = make_float2(-INFINITY, 0.f);
-            if (i < it.nparts) {
-                pr = attn_partial_row(p, Walk::owner(it.at, it.keys, share, i), i) + r;
-                ml = __ldcg(&p.ws_ml[pr]);
-            }
-            float mx = ml.x;
-#pragma unroll
-            for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-            const float Mn = fmaxf(M, mx);
-            const float alpha = Mn == -INFINITY ? 1.f : exp2f(M - Mn);
-            M = Mn;
-            L *= alpha;
-#pragma unroll
-            for (int e = 0; e < VE; ++e) acc[e] *= alpha;
-            // no key seen in any part: all sums are 0 (or NaN), taken as they are
-            const float w = Mn == -INFINITY ? 1.f : exp2f(ml.x - Mn);
-            const int count = it.nparts - i0 < 32 ? it.nparts - i0 : 32;
+    const int mine = warp + NW * lane;
+    float M = -INFINITY, L = 0.f;
+    if (mine < rows) {
 #pragma unroll 4
-            for (int j = 0; j < count; ++j) {
-                const float wj = __shfl_sync(0xffffffffu, w, j);
-                const long long prj = __shfl_sync(0xffffffffu, pr, j);
-                L = fmaf(wj, __shfl_sync(0xffffffffu, ml.y, j), L);
-                const float* o = p.ws_o + prj * D + lane * VE;
-                if constexpr (VE == 4) {
-                    const float4 v = __ldcg(reinterpret_cast<const float4*>(o));
-                    acc[0] = fmaf(wj, v.x, acc[0]);
-                    acc[1] = fmaf(wj, v.y, acc[1]);
-                    acc[2] = fmaf(wj, v.z, acc[2]);
-                    acc[3] = fmaf(wj, v.w, acc[3]);
-                } else {
-                    const float2 v = __ldcg(reinterpret_cast<const float2*>(o));
-                    acc[0] = fmaf(wj, v.x, acc[0]);
-                    acc[1] = fmaf(wj, v.y, acc[1]);
+        for (int i = 0; i < it.nparts; ++i)
+            M = fmaxf(M, __ldcg(&p.ws_ml[attn_partial_row(p, Walk::owner(it.at, it.keys, share, i), i) + mine]).x);
+#pragma unroll 4
+        for (int i = 0; i < it.nparts; ++i) {
+            const float2 ml = __ldcg(&p.ws_ml[attn_partial_row(p, Walk::owner(it.at, it.keys, share, i), i) + mine]);
+            // no key seen in any part: all sums are 0 (or NaN), taken as they are
+            L = fmaf(M == -INFINITY ? 1.f : exp2f(ml.x - M), ml.y, L);
+        }
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;  // no key seen: a zero row
+    for (int k0 = 0; warp + NW * k0 < rows; k0 += RB) {
+        float acc[RB][VE];
+#pragma unroll
+        for (int j = 0; j < RB; ++j)
+#pragma unroll
+            for (int e = 0; e < VE; ++e) acc[j][e] = 0.f;
+        for (int i0 = 0; i0 < it.nparts; i0 += PB) {
+            float w[PB], v[PB][RB][VE];
+#pragma unroll
+            for (int b = 0; b < PB; ++b) {
+                const int i = i0 + b;
+                const bool there = i < it.nparts;
+                const long long base = there ? attn_partial_row(p, Walk::owner(it.at, it.keys, share, i), i) : 0;
+                w[b] = 0.f;
+                if (there && mine < rows) {
+                    const float m = __ldcg(&p.ws_ml[base + mine]).x;
+                    w[b] = (M == -INFINITY ? 1.f : exp2f(m - M)) * inv;
+                }
+#pragma unroll
+                for (int j = 0; j < RB; ++j) {
+                    const int r = warp + NW * (k0 + j);
+                    const float* o = p.ws_o + (base + r) * D + lane * VE;
+                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (there && r < rows) {
+                        if constexpr (VE == 4) {
+                            x = __ldcg(reinterpret_cast<const float4*>(o));
+                        } else {
+                            const float2 y = __ldcg(reinterpret_cast<const float2*>(o));
+                            x = make_float4(y.x, y.y, 0.f, 0.f);
+                        }
+                    }
+                    v[b][j][0] = x.x;
+                    v[b][j][1] = x.y;
+                    if constexpr (VE == 4) {
+                        v[b][j][2] = x.z;
+                        v[b][j][3] = x.w;
+                    }
                 }
             }
-        }
-        const float inv = L == 0.f ? 0.f : 1.f / L;  // no key seen: a zero row
-        T* dst = static_cast<T*>(p.out) +
-                 ((long long)(it.row + (r >> p.group_log2)) * p.num_heads + it.g * G + (r & (G - 1))) * D + lane * VE;
 #pragma unroll
-        for (int e = 0; e < VE; ++e) Elem<T>::store(dst + e, acc[e] * inv);
+            for (int b = 0; b < PB; ++b)
+#pragma unroll
+                for (int j = 0; j < RB; ++j) {
+                    const float wj = __shfl_sync(0xffffffffu, w[b], k0 + j);
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) acc[j][e] = fmaf(wj, v[b][j][e], acc[j][e]);
+                }
+        }
+#pragma unroll
+        for (int j = 0; j < RB; ++j) {
+            const int r = warp + NW * (k0 + j);
+            if (r >= rows) continue;
+            T* dst = static_cast<T*>(p.out) +
+                     ((long long)(it.row + (r >> p.group_log2)) * p.num_heads + it.g * G + (r & (G - 1))) * D +
+                     lane * VE;
+#pragma unroll
+            for (int e = 0; e < VE; ++e) Elem<T>::store(dst + e, acc[j][e]);
+        }
     }
     return true;
 }

@@ -44,8 +44,6 @@ namespace pkv {
 namespace atc {
 
 using tc::fence_proxy_async_smem;
-using tc::mma_commit;
-using tc::mma_kind_f16;
 using tc::sw128_desc;
 using tc::tc_fence_after;
 using tc::tc_fence_before;
@@ -63,14 +61,43 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
         : "memory");
 }
 
-// D[tmem] (+)= A[tmem] . B[smem desc], 16-bit inputs, fp32 accumulator.
-__device__ __forceinline__ void mma_ts_f16(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                           uint32_t accumulate) {
+// One lane of a converged warp.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e;
+}
+
+// 16-bit MMAs with fp32 accumulators, by the lane with `one`: the whole warp
+// comes here with the same operands, which then stay in uniform registers (one
+// lane alone in a branch took 70 to 120 clocks for each instruction's
+// operands, longer than the 64 that the product itself takes).
+// D[tmem] (+)= A[smem desc] . B[smem desc]
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate, uint32_t one) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
+        : "memory");
+}
+// D[tmem] (+)= A[tmem] . B[smem desc]
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate, uint32_t one) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
+        : "memory");
+}
+// Arrive on `bar` when every MMA of the electing lane so far has completed.
+__device__ __forceinline__ void commit_one(uint64_t* bar, uint32_t one) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)),
+        "r"(one)
         : "memory");
 }
 
@@ -513,69 +540,71 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             }
         } else if (warp == 9) {
             // ------------------------------------------------------ MMA issue
-            if (lane == 0) {
-                const uint32_t q_base = smem_addr(smem + C::Q_OFF), s_base = smem_addr(smem + C::SLOT_OFF);
-                int base = 0;           // loads of the items before
-                int items_with_q = 0;
-                uint32_t p_phase[2] = {0, 0};
-                for (int n = 0;; ++n) {
-                    if (!wait(&item_full[n % C::ITEMS], (n / C::ITEMS) & 1)) break;
-                    const AttnItem u = *item_slot(n);
-                    mbar_arrive(&item_empty[n % C::ITEMS]);
-                    if (u.seq < 0) break;
-                    Plan plan;
-                    plan.set(u, gl);
-                    if (plan.steps == 0) continue;
-                    if (!wait(FP8 ? q_wide : q_full, items_with_q & 1)) break;
-                    ++items_with_q;
-                    mma_any = true;
-                    auto qk = [&](int i, int t) -> bool {
-                        const int j = plan.step(i, t), li = base + plan.k_load(j), st = li % C::NSLOT;
-                        if (!wait(&slot_full[st], (li / C::NSLOT) & 1)) return false;
-                        tc_fence_after();
-                        const uint32_t a0 = q_base + (plan.wide ? i : 0) * C::QTILE, b0 = s_base + st * C::TILE;
+            const uint32_t one = elect_one();
+            const uint32_t q_base = smem_addr(smem + C::Q_OFF), s_base = smem_addr(smem + C::SLOT_OFF);
+            // descriptors of the first tile; others differ in the address field (16-byte units)
+            const uint64_t q_desc = sw128_desc(q_base, 16, 1024), k_desc = sw128_desc(s_base, 16, C::GSTRIDE),
+                           v_desc = sw128_desc(s_base, C::HSTEP, C::GSTRIDE);
+            int base = 0;  // loads of the items before
+            int items_with_q = 0;
+            uint32_t p_phase[2] = {0, 0};
+            for (int n = 0;; ++n) {
+                if (!wait_warp(&item_full[n % C::ITEMS], (n / C::ITEMS) & 1)) break;
+                const AttnItem u = *item_slot(n);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&item_empty[n % C::ITEMS]);
+                if (u.seq < 0) break;
+                Plan plan;
+                plan.set(u, gl);
+                if (plan.steps == 0) continue;
+                if (!wait_warp(FP8 ? q_wide : q_full, items_with_q & 1)) break;
+                ++items_with_q;
+                mma_any = true;
+                auto qk = [&](int i, int t) -> bool {
+                    const int j = plan.step(i, t), li = base + plan.k_load(j), st = li % C::NSLOT;
+                    if (!wait_warp(&slot_full[st], (li / C::NSLOT) & 1)) return false;
+                    tc_fence_after();
+                    const uint64_t a0 = q_desc + (plan.wide ? i : 0) * (C::QTILE >> 4),
+                                   b0 = k_desc + st * (C::TILE >> 4);
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk)
-                            mma_kind_f16(tmem + i * 128,
-                                         sw128_desc(a0 + (kk >> 2) * C::QHALF + (kk & 3) * 32, 16, 1024),
-                                         sw128_desc(b0 + (kk >> 2) * C::HSTEP + (kk & 3) * 32, 16, C::GSTRIDE),
-                                         C::IDESC_QK, kk > 0);
-                        mma_commit(&s_full[i]);
-                        if (!plan.wide || i == 1) {
-                            mma_commit(&slot_empty[st]);
-                            if (j == plan.steps - 1) mma_commit(q_empty);
-                        }
-                        return true;
-                    };
-                    auto pv = [&](int i, int t) -> bool {
-                        const int j = plan.step(i, t), li = base + plan.v_load(j), st = li % C::NSLOT;
-                        if (!wait(&slot_full[st], (li / C::NSLOT) & 1)) return false;
-                        if (!wait(&p_full[i], p_phase[i])) return false;
-                        p_phase[i] ^= 1;
-                        tc_fence_after();
-                        const uint32_t b0 = s_base + st * C::TILE;
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        mma_ss(tmem + i * 128, a0 + (((kk >> 2) * C::QHALF + (kk & 3) * 32) >> 4),
+                               b0 + (((kk >> 2) * C::HSTEP + (kk & 3) * 32) >> 4), C::IDESC_QK, kk > 0, one);
+                    commit_one(&s_full[i], one);
+                    if (!plan.wide || i == 1) {
+                        commit_one(&slot_empty[st], one);
+                        if (j == plan.steps - 1) commit_one(q_empty, one);
+                    }
+                    return true;
+                };
+                auto pv = [&](int i, int t) -> bool {
+                    const int j = plan.step(i, t), li = base + plan.v_load(j), st = li % C::NSLOT;
+                    if (!wait_warp(&slot_full[st], (li / C::NSLOT) & 1)) return false;
+                    if (!wait_warp(&p_full[i], p_phase[i])) return false;
+                    p_phase[i] ^= 1;
+                    tc_fence_after();
+                    const uint64_t b0 = v_desc + st * (C::TILE >> 4);
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            mma_ts_f16(tmem + C::O_COL + i * 128, tmem + i * 128 + kk * 8,
-                                       sw128_desc(b0 + kk * 2 * C::GSTRIDE, C::HSTEP, C::GSTRIDE), C::IDESC_PV,
-                                       kk > 0 || t > 0);
-                        if (t == plan.n(i) - 1) mma_commit(&o_full[i]);
-                        if (!plan.wide || i == 1) mma_commit(&slot_empty[st]);
-                        return true;
-                    };
-                    bool ok = true;
-                    for (int i = 0; i < 2 && ok; ++i)
-                        if (plan.n(i) > 0) ok = qk(i, 0);
-                    const int nmax = plan.n0 > plan.n1 ? plan.n0 : plan.n1;
-                    for (int t = 0; t < nmax && ok; ++t)
-                        for (int i = 0; i < 2 && ok; ++i) {
-                            if (t >= plan.n(i)) continue;
-                            ok = pv(i, t);
-                            if (ok && t + 1 < plan.n(i)) ok = qk(i, t + 1);
-                        }
-                    if (!ok) break;
-                    base += 2 * plan.steps;
-                }
+                    for (int kk = 0; kk < 8; ++kk)
+                        mma_ts(tmem + C::O_COL + i * 128, tmem + i * 128 + kk * 8, b0 + ((kk * 2 * C::GSTRIDE) >> 4),
+                               C::IDESC_PV, kk > 0 || t > 0, one);
+                    if (t == plan.n(i) - 1) commit_one(&o_full[i], one);
+                    if (!plan.wide || i == 1) commit_one(&slot_empty[st], one);
+                    return true;
+                };
+                bool ok = true;
+                for (int i = 0; i < 2 && ok; ++i)
+                    if (plan.n(i) > 0) ok = qk(i, 0);
+                const int nmax = plan.n0 > plan.n1 ? plan.n0 : plan.n1;
+                for (int t = 0; t < nmax && ok; ++t)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (!ok || t >= plan.n(i)) continue;
+                        ok = pv(i, t);
+                        if (ok && t + 1 < plan.n(i)) ok = qk(i, t + 1);
+                    }
+                if (!ok) break;
+                base += 2 * plan.steps;
             }
         }
     } else if (warp < 8) {
@@ -980,8 +1009,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 land(&load_full[li % C::NLOAD], (li / C::NLOAD) & 1);
             if (q_loads > 0) land(q_full, (q_loads - 1) & 1);
         }
-        if (warp == 9 && lane == 0 && mma_any) {
-            mma_commit(mma_done);
+        if (warp == 9 && mma_any) {
+            commit_one(mma_done, elect_one());
             land(mma_done, 0);
         }
         // parts that were not counted: empty ones, so that the counters end at zero
