@@ -61,6 +61,42 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
         : "memory");
 }
 
+// Barriers by their shared-memory address.
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(bar),
+                 "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// Rest of a warp's wait whose first look was in vain: false when it ran out
+// of time or another warp has given up.
+__device__ __forceinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                           unsigned long long wait_ns, int* err) {
+    const unsigned long long t0 = globaltimer_ns();
+    for (;;) {
+        if (__all_sync(0xffffffffu, bar_try(bar, parity))) return true;
+        const bool late = globaltimer_ns() - t0 > wait_ns;
+        if (__any_sync(0xffffffffu, late || *abort_flag)) {
+            if ((threadIdx.x & 31) == 0) {
+                set_error(err, PKV_ERR_TIMEOUT);
+                *abort_flag = 1;
+            }
+            return false;
+        }
+    }
+}
+
 // One lane of a converged warp.
 __device__ __forceinline__ uint32_t elect_one() {
     uint32_t e;
@@ -71,32 +107,35 @@ __device__ __forceinline__ uint32_t elect_one() {
 // 16-bit MMAs with fp32 accumulators, by the lane with `one`: the whole warp
 // comes here with the same operands, which then stay in uniform registers (one
 // lane alone in a branch took 70 to 120 clocks for each instruction's
-// operands, longer than the 64 that the product itself takes).
+// operands, longer than the 64 that the product itself takes).  Descriptors
+// come as their two words: only the low one, with the address, varies.
 // D[tmem] (+)= A[smem desc] . B[smem desc]
-__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                       uint32_t accumulate, uint32_t one) {
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                       uint32_t idesc, uint32_t accumulate, uint32_t one) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(one)
         : "memory");
 }
 // D[tmem] (+)= A[tmem] . B[smem desc]
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
                                        uint32_t accumulate, uint32_t one) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(one)
         : "memory");
 }
 // Arrive on `bar` when every MMA of the electing lane so far has completed.
-__device__ __forceinline__ void commit_one(uint64_t* bar, uint32_t one) {
+__device__ __forceinline__ void commit_one(uint32_t bar, uint32_t one) {
     asm volatile(
         "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)),
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
         "r"(one)
         : "memory");
 }
@@ -128,6 +167,15 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
 
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
 
 template <int REGS>
 __device__ __forceinline__ void regs_inc() {
@@ -165,6 +213,31 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return d;
 }
 
+// max(a, b, c), NaN if any of them is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// 2^x of two values up to 127 (0 below -125) on the FMA pipe: x = n + f with n
+// the nearest integer and |f| <= 1/2, 2^f by the polynomial of degree 3 with
+// the least relative error there (an exchange algorithm's; 7.5e-5, a thirtieth
+// of bf16's half step), n added to the exponent.  Not for NaN.
+__device__ __forceinline__ float2 ex2_poly(float2 x) {
+    const float2 big = make_float2(12582912.f, 12582912.f), neg = make_float2(-12582912.f, -12582912.f);
+    const float2 t = add2(x, big);  // 1.5 2^23 + n: n in the low bits
+    const float2 n = add2(t, neg);
+    const float2 f = fma2(n, make_float2(-1.f, -1.f), x);
+    float2 y = fma2(f, make_float2(0.0551716685295105f, 0.0551716685295105f),
+                    make_float2(0.2426111251115799f, 0.2426111251115799f));
+    y = fma2(y, f, make_float2(0.6932609677314758f, 0.6932609677314758f));
+    y = fma2(y, f, make_float2(0.9999280571937561f, 0.9999280571937561f));
+    y.x = x.x < -125.f ? 0.f : __uint_as_float(__float_as_uint(y.x) + (__float_as_uint(t.x) << 23));
+    y.y = x.y < -125.f ? 0.f : __uint_as_float(__float_as_uint(y.y) + (__float_as_uint(t.y) << 23));
+    return y;
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -174,6 +247,44 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// Weights 2^(x q + m) of the pairs [C0, C0 + CN) of a row's scores, packed for
+// the MMA; sum gets their total.  One pair in POLY_OF goes by ex2_poly, so that
+// the special-function unit (a quarter of the lanes a clock) and the FMA pipe
+// share the work.
+constexpr int POLY_OF = 4;
+template <bool FP8, int C0, int CN>
+__device__ __forceinline__ void weights(const float* x, float2 q, float2 m, uint32_t* pk, float2& sum) {
+    float2 sum1 = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int c = C0; c < C0 + CN; ++c) {
+        float2 y = fma2(make_float2(x[2 * c], x[2 * c + 1]), q, m);
+        if (c % POLY_OF == POLY_OF - 1) {
+            y = ex2_poly(y);
+        } else {
+            y.x = ex2(y.x);
+            y.y = ex2(y.y);
+        }
+        if (c & 1) sum1 = add2(sum1, y); else sum = add2(sum, y);
+        pk[c - C0] = FP8 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
+    }
+    sum = add2(sum, sum1);
+}
+
+// Largest of a row's scores; NaN if any of them is.
+__device__ __forceinline__ float largest(const float* x) {
+    float m0 = x[0], m1 = x[1], m2 = x[2], m3 = x[3];
+#pragma unroll
+    for (int c = 4; c < 124; c += 8) {
+        m0 = max3_nan(m0, x[c], x[c + 1]);
+        m1 = max3_nan(m1, x[c + 2], x[c + 3]);
+        m2 = max3_nan(m2, x[c + 4], x[c + 5]);
+        m3 = max3_nan(m3, x[c + 6], x[c + 7]);
+    }
+    m0 = max3_nan(m0, x[124], x[125]);
+    m1 = max3_nan(m1, x[126], x[127]);
+    return max3_nan(max3_nan(m0, m1, m2), m3, m3);
 }
 
 // ---------------------------------------------------------------- geometry
@@ -217,8 +328,17 @@ struct Cfg {
     static constexpr int RAW_OFF = SLOT_OFF + NSLOT * TILE;
     static constexpr int BAR_OFF = RAW_OFF + NRAW * RAW;
     // full/empty of the load ring, of the widened ring, q_full q_empty q_wide,
-    // s_full[2] p_full[2] o_full[2], x_full x_empty, item full/empty, sync, mma_done
-    static constexpr int NBARS = 2 * NLOAD + (FP8 ? 2 * NSLOT : 0) + 3 + 6 + 2 + 2 * ITEMS + 2;
+    // s_full[2] p_full[2] p_rest[2] o_full[2], x_full x_empty, item full/empty, sync, mma_done
+    static constexpr int NBARS = 2 * NLOAD + (FP8 ? 2 * NSLOT : 0) + 3 + 8 + 2 + 2 * ITEMS + 2;
+    static constexpr int LOAD_FULL = BAR_OFF, LOAD_EMPTY = LOAD_FULL + 8 * NLOAD;
+    static constexpr int SLOT_FULL = FP8 ? LOAD_EMPTY + 8 * NLOAD : LOAD_FULL;  // what the MMA waits for
+    static constexpr int SLOT_EMPTY = FP8 ? SLOT_FULL + 8 * NSLOT : LOAD_EMPTY;
+    static constexpr int Q_FULL = SLOT_EMPTY + 8 * NSLOT, Q_EMPTY = Q_FULL + 8, Q_WIDE = Q_FULL + 16;
+    static constexpr int S_FULL = Q_FULL + 24, P_FULL = S_FULL + 16, P_REST = S_FULL + 32, O_FULL = S_FULL + 48;
+    static constexpr int X_FULL = S_FULL + 64, X_EMPTY = X_FULL + 8;
+    static constexpr int ITEM_FULL = X_EMPTY + 8, ITEM_EMPTY = ITEM_FULL + 8 * ITEMS;
+    static constexpr int SYNC_BAR = ITEM_EMPTY + 8 * ITEMS, MMA_DONE = SYNC_BAR + 8;
+    static_assert(MMA_DONE + 8 == BAR_OFF + NBARS * 8, "");
     static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;  // tmem address, abort, flag, turns
     static constexpr int ITEM_OFF = (MISC_OFF + 16 + 15) / 16 * 16;
     static constexpr int WALK_OFF = ITEM_OFF + ITEMS * 64;
@@ -363,23 +483,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     using C = Cfg<D, FP8>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
-    uint64_t* load_full = bars;
-    uint64_t* load_empty = load_full + C::NLOAD;
-    uint64_t* slot_full = FP8 ? load_empty + C::NLOAD : load_full;  // what the MMA waits for
-    uint64_t* slot_empty = FP8 ? slot_full + C::NSLOT : load_empty;
-    uint64_t* q_full = slot_empty + C::NSLOT;
-    uint64_t* q_empty = q_full + 1;
-    uint64_t* q_wide = q_full + 2;
-    uint64_t* s_full = q_full + 3;
-    uint64_t* p_full = s_full + 2;
-    uint64_t* o_full = s_full + 4;
-    uint64_t* x_full = s_full + 6;
-    uint64_t* x_empty = s_full + 7;
-    uint64_t* item_full = s_full + 8;
-    uint64_t* item_empty = item_full + C::ITEMS;
-    uint64_t* sync_bar = item_empty + C::ITEMS;
-    uint64_t* mma_done = sync_bar + 1;
+    const uint32_t sb = smem_addr(smem);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
     int* merge_flag = reinterpret_cast<int*>(smem + C::MISC_OFF + 8);
@@ -389,32 +493,34 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
+        auto init = [&](int off, uint32_t count) { mbar_init(reinterpret_cast<uint64_t*>(smem + off), count); };
         for (int i = 0; i < C::NLOAD; ++i) {
-            mbar_init(&load_full[i], 1);
-            mbar_init(&load_empty[i], FP8 ? 4 : 1);
+            init(C::LOAD_FULL + 8 * i, 1);
+            init(C::LOAD_EMPTY + 8 * i, FP8 ? 4 : 1);
         }
         if constexpr (FP8) {
             for (int i = 0; i < C::NSLOT; ++i) {
-                mbar_init(&slot_full[i], 4);
-                mbar_init(&slot_empty[i], 1);
+                init(C::SLOT_FULL + 8 * i, 4);
+                init(C::SLOT_EMPTY + 8 * i, 1);
             }
         }
-        mbar_init(q_full, 1);
-        mbar_init(q_empty, FP8 ? 9 : 1);  // the last QK^T, fp8: and the softmax warps have the rows' scales
-        mbar_init(q_wide, 4);
+        init(C::Q_FULL, 1);
+        init(C::Q_EMPTY, FP8 ? 9 : 1);  // the last QK^T, fp8: and the softmax warps have the rows' scales
+        init(C::Q_WIDE, 4);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);
-            mbar_init(&o_full[i], 1);
+            init(C::S_FULL + 8 * i, 1);
+            init(C::P_FULL + 8 * i, 4);
+            init(C::P_REST + 8 * i, 4);
+            init(C::O_FULL + 8 * i, 1);
         }
-        mbar_init(x_full, 4);
-        mbar_init(x_empty, 4);
+        init(C::X_FULL, 4);
+        init(C::X_EMPTY, 4);
         for (int i = 0; i < C::ITEMS; ++i) {
-            mbar_init(&item_full[i], 1);
-            mbar_init(&item_empty[i], 10 + (FP8 ? 4 : 0));  // producer, MMA, softmax and widening warps
+            init(C::ITEM_FULL + 8 * i, 1);
+            init(C::ITEM_EMPTY + 8 * i, 10 + (FP8 ? 4 : 0));  // producer, MMA, softmax and widening warps
         }
-        mbar_init(sync_bar, 8);
-        mbar_init(mma_done, 1);
+        init(C::SYNC_BAR, 8);
+        init(C::MMA_DONE, 1);
         *abort_flag = 0;
         *turns = 0;
         fence_mbarrier_init();
@@ -434,24 +540,24 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     const int bpt = C::KEYS / bs;  // blocks of a step
     const int bl = 31 - __clz(bs);
 
-    // A wait by the whole warp (or by the one lane that is there); false: wind down.
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-        if (mbar_wait_bounded(bar, parity, abort_flag, p.wait_ns)) return true;
-        set_error(p.err, PKV_ERR_TIMEOUT);
-        *abort_flag = 1;
-        return false;
+    // A wait by a converged warp; false: wind down.
+    auto wait = [&](uint32_t off, uint32_t parity) -> bool {
+        if (__all_sync(0xffffffffu, bar_try(sb + off, parity))) return true;
+        return bar_wait_slow(sb + off, parity, abort_flag, p.wait_ns, p.err);
     };
-    auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool {
-        const bool ok = mbar_wait_bounded(bar, parity, abort_flag, p.wait_ns);
-        if (__all_sync(0xffffffffu, ok)) return true;
-        if (lane == 0) {
-            set_error(p.err, PKV_ERR_TIMEOUT);
-            *abort_flag = 1;
-        }
-        return false;
+    auto arrive = [&](uint32_t off) {  // once for the warp, after what its lanes did
+        __syncwarp();
+        if (lane == 0) bar_arrive(sb + off);
     };
-    // Item n of the CTA, as the walk put it into the ring (seq < 0: no more).
-    auto item_slot = [&](int n) { return reinterpret_cast<AttnItem*>(smem + C::ITEM_OFF + (n % C::ITEMS) * 64); };
+    // Items in the order in which the walk puts them into the ring; false: no more, or wind down.
+    static_assert((C::ITEMS & (C::ITEMS - 1)) == 0, "");
+    auto take_item = [&](int n, AttnItem& u) -> bool {
+        const uint32_t i = n & (C::ITEMS - 1);
+        if (!wait(C::ITEM_FULL + 8 * i, (n / C::ITEMS) & 1)) return false;
+        u = *reinterpret_cast<const AttnItem*>(smem + C::ITEM_OFF + i * 64);
+        arrive(C::ITEM_EMPTY + 8 * i);
+        return u.seq >= 0;
+    };
 
     int loads = 0;  // producer: copies issued; of Q: items
     int q_loads = 0;
@@ -461,44 +567,32 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
         regs_dec<C::REGS_ISSUE>();
         if (warp == 10) {
             // ------------------------------------------------------- the walk
-            if (lane == 0) {
-                AttnWalk<TcDivision> walk = walk0;
-                for (int n = 0;; ++n) {
-                    if (n >= C::ITEMS && !wait(&item_empty[n % C::ITEMS], (n / C::ITEMS - 1) & 1)) break;
-                    AttnItem u;
-                    const bool more = walk.next(p, u);
-                    if (!more) u.seq = -1;
-                    *item_slot(n) = u;
-                    mbar_arrive(&item_full[n % C::ITEMS]);
-                    if (!more) break;
-                }
+            AttnWalk<TcDivision> walk = walk0;
+            for (int n = 0;; ++n) {
+                const uint32_t i = n & (C::ITEMS - 1);
+                if (n >= C::ITEMS && !wait(C::ITEM_EMPTY + 8 * i, (n / C::ITEMS - 1) & 1)) break;
+                AttnItem u;
+                const bool more = walk.next(p, u);
+                if (!more) u.seq = -1;
+                if (lane == 0) *reinterpret_cast<AttnItem*>(smem + C::ITEM_OFF + i * 64) = u;
+                arrive(C::ITEM_FULL + 8 * i);
+                if (!more) break;
             }
         } else if (warp == 8) {
             // ------------------------------------------------------- producer
-            for (int n = 0;; ++n) {
-                if (!wait_warp(&item_full[n % C::ITEMS], (n / C::ITEMS) & 1)) break;
-                const AttnItem u = *item_slot(n);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&item_empty[n % C::ITEMS]);
-                if (u.seq < 0) break;
+            uint32_t st = 0, phase = 1;  // slot, parity of its emptying (the first round finds them empty)
+            AttnItem u;
+            for (int n = 0; take_item(n, u); ++n) {
                 Plan plan;
                 plan.set(u, gl);
                 if (plan.steps == 0) continue;
-                if (q_loads > 0 && !wait_warp(q_empty, (q_loads - 1) & 1)) break;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(q_full, (plan.wide ? 2 : 1) * C::QTILE);
-                    for (int t = 0; t < (plan.wide ? 2 : 1); ++t)
-                        for (int h = 0; h < C::HALVES; ++h)
-                            tma_load_3d(smem + C::Q_OFF + t * C::QTILE + h * C::QHALF, &tmq, h * 64, u.g * G,
-                                        u.row + t * (128 >> gl), q_full);
-                }
-                ++q_loads;
                 const int32_t* bt = p.block_tables + (long long)u.seq * p.max_blocks_per_seq;
+                const int n_loads = 2 * plan.steps;
                 auto entry = [&](int l) {  // lane j: block j of load l
                     bool v;
-                    if (l >= 2 * plan.steps) return -1;
+                    if (l >= n_loads || lane >= bpt) return -1;
                     const int key = u.kv0 + plan.load_step(l, v) * C::KEYS + lane * bs;
-                    if (lane >= bpt || key >= u.kv1) return -1;
+                    if (key >= u.kv1) return -1;
                     const int e = __ldg(bt + (key >> bl));
                     if (e >= 0 && e < p.num_blocks) return e;
                     set_error(p.err, PKV_ERR_DEVICE_BOUNDS);
@@ -506,105 +600,155 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 };
                 int e = entry(0), e1 = entry(1);
                 bool ok = true;
-                for (int l = 0; l < 2 * plan.steps; ++l) {
+                for (int l = 0; l < n_loads; ++l) {
                     const int e2 = entry(l + 2);  // two loads ahead of its use
-                    const int st = loads % C::NLOAD;
-                    if (loads >= C::NLOAD && !wait_warp(&load_empty[st], (loads / C::NLOAD - 1) & 1)) {
-                        ok = false;
-                        break;
-                    }
+                    if (!(ok = wait(C::LOAD_EMPTY + 8 * st, phase))) break;
                     bool v;
                     plan.load_step(l, v);
+                    const uint32_t full = sb + C::LOAD_FULL + 8 * st;
                     const int count = __popc(__ballot_sync(0xffffffffu, e >= 0));
                     if (lane == 0) {
                         if (count > 0)
-                            mbar_arrive_expect_tx(&load_full[st], (uint32_t)(count * bs * D * (FP8 ? 1 : 2)));
+                            bar_expect(full, (uint32_t)(count * bs * D * (FP8 ? 1 : 2)));
                         else
-                            mbar_arrive(&load_full[st]);
+                            bar_arrive(full);
                     }
                     __syncwarp();  // the expected byte count is registered before any copy lands
                     if (e >= 0) {
                         const CUtensorMap* map = v ? &tmv : &tmk;
+                        uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::LOAD_FULL + 8 * st);
                         if constexpr (FP8)
-                            tma_load_3d(smem + C::RAW_OFF + st * C::RAW + lane * bs * D, map, 0, 0, e * Hkv + u.g,
-                                        &load_full[st]);
+                            tma_load_3d(smem + C::RAW_OFF + st * C::RAW + lane * bs * D, map, 0, 0, e * Hkv + u.g, bar);
                         else
                             tma_load_5d(smem + C::SLOT_OFF + st * C::TILE + lane * bs * D * 2, map, 0, 0, 0, 0,
-                                        e * Hkv + u.g, &load_full[st]);
+                                        e * Hkv + u.g, bar);
                     }
                     ++loads;
+                    if (++st == C::NLOAD) st = 0, phase ^= 1;
                     e = e1;
                     e1 = e2;
+                    if (l == 1) {
+                        // Q after the first K and V: its space is free only after the item before
+                        if (q_loads > 0 && !(ok = wait(C::Q_EMPTY, (q_loads - 1) & 1))) break;
+                        if (lane == 0) {
+                            bar_expect(sb + C::Q_FULL, (plan.wide ? 2 : 1) * C::QTILE);
+                            for (int t = 0; t < (plan.wide ? 2 : 1); ++t)
+                                for (int h = 0; h < C::HALVES; ++h)
+                                    tma_load_3d(smem + C::Q_OFF + t * C::QTILE + h * C::QHALF, &tmq, h * 64, u.g * G,
+                                                u.row + t * (128 >> gl), reinterpret_cast<uint64_t*>(smem + C::Q_FULL));
+                        }
+                        ++q_loads;
+                    }
                 }
                 if (!ok) break;
             }
         } else if (warp == 9) {
             // ------------------------------------------------------ MMA issue
+            // Every instruction here counts: between two products the tensor cores
+            // wait for this warp, whose instructions are fetched anew each time.
             const uint32_t one = elect_one();
-            const uint32_t q_base = smem_addr(smem + C::Q_OFF), s_base = smem_addr(smem + C::SLOT_OFF);
             // descriptors of the first tile; others differ in the address field (16-byte units)
-            const uint64_t q_desc = sw128_desc(q_base, 16, 1024), k_desc = sw128_desc(s_base, 16, C::GSTRIDE),
-                           v_desc = sw128_desc(s_base, C::HSTEP, C::GSTRIDE);
-            int base = 0;  // loads of the items before
-            int items_with_q = 0;
-            uint32_t p_phase[2] = {0, 0};
-            for (int n = 0;; ++n) {
-                if (!wait_warp(&item_full[n % C::ITEMS], (n / C::ITEMS) & 1)) break;
-                const AttnItem u = *item_slot(n);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&item_empty[n % C::ITEMS]);
-                if (u.seq < 0) break;
+            const uint64_t q_desc = sw128_desc(sb + C::Q_OFF, 16, 1024),
+                           k_desc = sw128_desc(sb + C::SLOT_OFF, 16, C::GSTRIDE),
+                           v_desc = sw128_desc(sb + C::SLOT_OFF, C::HSTEP, C::GSTRIDE);
+            const uint32_t q_lo = (uint32_t)q_desc, q_hi = (uint32_t)(q_desc >> 32), k_lo = (uint32_t)k_desc,
+                           k_hi = (uint32_t)(k_desc >> 32), v_lo = (uint32_t)v_desc, v_hi = (uint32_t)(v_desc >> 32);
+            // a negative scale turns the order of the scores: they are taken with A negated
+            const uint32_t idesc_qk = C::IDESC_QK | (p.qscale < 0.f ? 1u << 13 : 0u);
+            uint32_t slot = 0, slot_phase = 0;  // loads are used in their order
+            uint32_t q_phase = 0, p_phase0 = 0, p_phase1 = 0;
+            bool ok = true;
+            auto next_load = [&]() -> uint32_t {
+                const uint32_t st = slot;
+                ok = ok && wait(C::SLOT_FULL + 8 * st, slot_phase);
+                if (++slot == C::NSLOT) slot = 0, slot_phase ^= 1;
+                return st;
+            };
+            auto qk = [&](int i, uint32_t q_tile, uint32_t st) {
+                const uint32_t a = q_lo + q_tile * (C::QTILE >> 4), b = k_lo + st * (C::TILE >> 4);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    mma_ss(tmem + i * 128, a + (((kk >> 2) * C::QHALF + (kk & 3) * 32) >> 4), q_hi,
+                           b + (((kk >> 2) * C::HSTEP + (kk & 3) * 32) >> 4), k_hi, idesc_qk, kk > 0, one);
+                commit_one(sb + C::S_FULL + 8 * i, one);
+            };
+            auto pv = [&](int i, uint32_t st, uint32_t phase, uint32_t accumulate) {
+                const uint32_t b = v_lo + st * (C::TILE >> 4);
+                ok = ok && wait(C::P_FULL + 8 * i, phase);
+                if (!ok) return;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) {
+                    if (kk == 6) {
+                        if (!(ok = wait(C::P_REST + 8 * i, phase))) return;
+                        tc_fence_after();
+                    }
+                    mma_ts(tmem + C::O_COL + i * 128, tmem + i * 128 + kk * 8, b + ((kk * 2 * C::GSTRIDE) >> 4), v_hi,
+                           C::IDESC_PV, kk > 0 ? 1u : accumulate, one);
+                }
+            };
+            AttnItem u;
+            for (int n = 0; ok && take_item(n, u); ++n) {
                 Plan plan;
                 plan.set(u, gl);
                 if (plan.steps == 0) continue;
-                if (!wait_warp(FP8 ? q_wide : q_full, items_with_q & 1)) break;
-                ++items_with_q;
+                const bool wide = plan.wide;
+                const int n0 = plan.n0, n1 = plan.n1;
+                if (!(ok = wait(FP8 ? C::Q_WIDE : C::Q_FULL, q_phase))) break;
+                q_phase ^= 1;
                 mma_any = true;
-                auto qk = [&](int i, int t) -> bool {
-                    const int j = plan.step(i, t), li = base + plan.k_load(j), st = li % C::NSLOT;
-                    if (!wait_warp(&slot_full[st], (li / C::NSLOT) & 1)) return false;
-                    tc_fence_after();
-                    const uint64_t a0 = q_desc + (plan.wide ? i : 0) * (C::QTILE >> 4),
-                                   b0 = k_desc + st * (C::TILE >> 4);
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk)
-                        mma_ss(tmem + i * 128, a0 + (((kk >> 2) * C::QHALF + (kk & 3) * 32) >> 4),
-                               b0 + (((kk >> 2) * C::HSTEP + (kk & 3) * 32) >> 4), C::IDESC_QK, kk > 0, one);
-                    commit_one(&s_full[i], one);
-                    if (!plan.wide || i == 1) {
-                        commit_one(&slot_empty[st], one);
-                        if (j == plan.steps - 1) commit_one(q_empty, one);
-                    }
-                    return true;
-                };
-                auto pv = [&](int i, int t) -> bool {
-                    const int j = plan.step(i, t), li = base + plan.v_load(j), st = li % C::NSLOT;
-                    if (!wait_warp(&slot_full[st], (li / C::NSLOT) & 1)) return false;
-                    if (!wait_warp(&p_full[i], p_phase[i])) return false;
-                    p_phase[i] ^= 1;
-                    tc_fence_after();
-                    const uint64_t b0 = v_desc + st * (C::TILE >> 4);
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        mma_ts(tmem + C::O_COL + i * 128, tmem + i * 128 + kk * 8, b0 + ((kk * 2 * C::GSTRIDE) >> 4),
-                               C::IDESC_PV, kk > 0 || t > 0, one);
-                    if (t == plan.n(i) - 1) commit_one(&o_full[i], one);
-                    if (!plan.wide || i == 1) commit_one(&slot_empty[st], one);
-                    return true;
-                };
-                bool ok = true;
-                for (int i = 0; i < 2 && ok; ++i)
-                    if (plan.n(i) > 0) ok = qk(i, 0);
-                const int nmax = plan.n0 > plan.n1 ? plan.n0 : plan.n1;
-                for (int t = 0; t < nmax && ok; ++t)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (!ok || t >= plan.n(i)) continue;
-                        ok = pv(i, t);
-                        if (ok && t + 1 < plan.n(i)) ok = qk(i, t + 1);
-                    }
+                int left = plan.steps;  // K tiles not used up yet
+                uint32_t ks = next_load(), vs = 0;
                 if (!ok) break;
-                base += 2 * plan.steps;
+                tc_fence_after();
+                if (n0 > 0) qk(0, 0, ks);
+                if (!wide) {
+                    commit_one(sb + C::SLOT_EMPTY + 8 * ks, one);
+                    --left;
+                    if (n1 > 0) ks = next_load();
+                    if (!ok) break;
+                }
+                if (n1 > 0) {
+                    qk(1, wide, ks);
+                    commit_one(sb + C::SLOT_EMPTY + 8 * ks, one);
+                    --left;
+                }
+                if (left == 0) commit_one(sb + C::Q_EMPTY, one);
+                const int nmax = n0 > n1 ? n0 : n1;
+                for (int t = 0; t < nmax; ++t) {
+                    if (t < n0) {
+                        vs = next_load();
+                        if (t + 1 < n0) ks = next_load();
+                        pv(0, vs, p_phase0, t > 0);
+                        if (!ok) break;
+                        p_phase0 ^= 1;
+                        if (!wide) commit_one(sb + C::SLOT_EMPTY + 8 * vs, one);
+                        if (t + 1 < n0) {
+                            qk(0, 0, ks);
+                            if (!wide) {
+                                commit_one(sb + C::SLOT_EMPTY + 8 * ks, one);
+                                if (--left == 0) commit_one(sb + C::Q_EMPTY, one);
+                            }
+                        } else {
+                            commit_one(sb + C::O_FULL, one);
+                        }
+                    }
+                    if (t < n1) {
+                        if (!wide || t >= n0) vs = next_load();
+                        if (t + 1 < n1 && (!wide || t + 1 >= n0)) ks = next_load();
+                        pv(1, vs, p_phase1, t > 0);
+                        if (!ok) break;
+                        p_phase1 ^= 1;
+                        commit_one(sb + C::SLOT_EMPTY + 8 * vs, one);
+                        if (t + 1 < n1) {
+                            qk(1, wide, ks);
+                            commit_one(sb + C::SLOT_EMPTY + 8 * ks, one);
+                            if (--left == 0) commit_one(sb + C::Q_EMPTY, one);
+                        } else {
+                            commit_one(sb + C::O_FULL + 8, one);
+                        }
+                    }
+                }
             }
         }
     } else if (warp < 8) {
@@ -615,23 +759,24 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
         const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t t_s = t_lane + wg * 128, t_o = t_lane + C::O_COL + wg * 128;
         int base = 0;                  // loads of the items before
-        uint32_t s_phase = 0, o_phase[2] = {0, 0}, x_phase = 0, sync_phase = 0;
+        uint32_t s_phase = 0, o_phase[2] = {0, 0}, x_phase = 0, sync_phase = 0, q_phase = 0;
         bool x_pending = false;        // WG 1: its O has not been read yet
-        int q_items = 0;
         bool ok = true;
         auto sync = [&]() -> bool {    // all 256 threads
-            __syncwarp();
-            if (lane == 0) mbar_arrive(sync_bar);
-            const bool s = wait_warp(sync_bar, sync_phase);
+            arrive(C::SYNC_BAR);
+            const bool s = wait(C::SYNC_BAR, sync_phase);
             sync_phase ^= 1;
             return s;
         };
-        for (int n = 0; ok; ++n) {
-            if (!(ok = wait_warp(&item_full[n % C::ITEMS], (n / C::ITEMS) & 1))) break;
-            const AttnItem u = *item_slot(n);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&item_empty[n % C::ITEMS]);
-            if (u.seq < 0) break;
+        auto o_readable = [&]() -> bool {  // the item before: O of this pipeline has been read
+            if (!x_pending) return true;
+            x_pending = false;
+            const bool r = wait(C::X_EMPTY, x_phase);
+            x_phase ^= 1;
+            return r;
+        };
+        AttnItem u;
+        for (int n = 0; ok && take_item(n, u); ++n) {
             Plan plan;
             plan.set(u, gl);
             const int rows = u.ntok << gl;
@@ -646,14 +791,16 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             if constexpr (FP8) {
                 qs *= p.k_scales[u.g];
                 if (plan.steps > 0) {
-                    if (!(ok = wait_warp(q_wide, q_items & 1))) break;
-                    ++q_items;
+                    if (!(ok = wait(C::Q_WIDE, q_phase))) break;
+                    q_phase ^= 1;
                     qs *= __uint_as_float((uint32_t)q_row_scale[row] << 23);
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(q_empty);
+                    arrive(C::Q_EMPTY);
                 }
             }
-            const bool negate = qs < 0.f;  // a negative scale turns the order of the scores
+            // (a negative scale: the scores come negated.)  A scale of 0 weighs what is
+            // seen alike, and -inf * 0 is not -inf
+            const float qa = fmaxf(fabsf(qs), __uint_as_float(1u));
+            const float2 q2 = make_float2(qa, qa);
             // keys that every row of the warp sees
             const int row0 = (plan.wide ? wg * 128 : 0) + (warp & 3) * 32;
             const int clear = par ? u.first : u.pos + (row0 >> gl) + 1;
@@ -668,29 +815,30 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 const int j = plan.step(wg, t), k0 = u.kv0 + j * C::KEYS;
                 const uint32_t bad = __ballot_sync(0xffffffffu, e_next < 0 || e_next >= p.num_blocks);
                 e_next = entry(t + 1);
-                if (!(ok = wait_warp(&s_full[wg], s_phase))) break;
+                if (!(ok = wait(C::S_FULL + 8 * wg, s_phase))) break;
                 s_phase ^= 1;
                 tc_fence_after();
                 float x[128];
+                auto scores = [&]() {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, x + 32 * c);
-                tmem_wait_ld();
-                if (negate) {
-#pragma unroll
-                    for (int c = 0; c < 128; ++c) x[c] = -x[c];
-                }
+                    for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, x + 32 * c);
+                    tmem_wait_ld();
+                };
+                scores();
                 const bool short_step = k0 + C::KEYS > u.kv1 || bad != 0;
-                if (short_step || k0 + C::KEYS > clear) {
+                const bool masked = short_step || k0 + C::KEYS > clear;
+                if (masked) {
                     uint32_t w[4], there[4];
                     seen_words(par, u.first, qi, k0, w);
                     there_words(u.kv1 - k0, bad, bs, there);
 #pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (!(w[c >> 5] & there[c >> 5] & (1u << (c & 31)))) x[c] = -INFINITY;
+                    for (int c = 0; c < 4; ++c) w[c] &= there[c];
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) x[c] = w[c >> 5] & (1u << (c & 31)) ? x[c] : -INFINITY;
                     if (!FP8 && short_step && (!plan.wide || wg == 0 || j >= plan.n0)) {
                         // keys that are not there: their rows of V may hold anything
                         const int li = base + plan.v_load(j), st = li % C::NSLOT;
-                        if (!(ok = wait_warp(&slot_full[st], (li / C::NSLOT) & 1))) break;
+                        if (!(ok = wait(C::SLOT_FULL + 8 * st, (li / C::NSLOT) & 1))) break;
                         const uint32_t word = lane_row < 32 ? there[0] : lane_row < 64 ? there[1]
                                               : lane_row < 96 ? there[2] : there[3];
                         if (!(word >> (lane_row & 31) & 1)) {
@@ -705,92 +853,81 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                         fence_proxy_async_smem();
                     }
                 }
-                // a scale of 0 weighs what is seen alike, and -inf * 0 is not -inf
-                const float qa = fmaxf(fabsf(qs), __uint_as_float(1u));
-                float mx0 = x[0], mx1 = x[1], mx2 = x[2], mx3 = x[3];
+                uint32_t pk[48];
+                float2 sum;
+                // The old maximum does for a step that does not exceed it by more than 2^8,
+                // as hardly any does once an item has begun: the weights are taken with it
+                // while the new one is still being found, and are taken again if it does not.
+                for (bool exact = masked || t == 0;; exact = true) {
+                    if (exact) {
+                        float mx = largest(x) * qa;
+                        if (__any_sync(0xffffffffu, !(mx <= m + (8.f + C::SHIFT)))) {
+                            // a score that is NaN or infinite: a row of NaN, for slow_row
+                            if (!(mx < INFINITY)) mx = __uint_as_float(0x7fffffffu);
+                            const float mn = mx - C::SHIFT > m || mx != mx ? mx - C::SHIFT : m;
+                            const float alpha = mn == -INFINITY ? 1.f : ex2(m - mn);
+                            m = mn;
+                            l *= alpha;
+                            if (t > 0) {  // s_full: the product before this step's scores is complete
 #pragma unroll
-                for (int c = 4; c < 124; c += 8) {
-                    mx0 = fmaxf(fmaxf(mx0, x[c]), x[c + 1]);
-                    mx1 = fmaxf(fmaxf(mx1, x[c + 2]), x[c + 3]);
-                    mx2 = fmaxf(fmaxf(mx2, x[c + 4]), x[c + 5]);
-                    mx3 = fmaxf(fmaxf(mx3, x[c + 6]), x[c + 7]);
-                }
-                mx0 = fmaxf(fmaxf(mx0, x[124]), x[125]);
-                mx1 = fmaxf(fmaxf(mx1, x[126]), x[127]);
-                const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * qa;
-                if (__any_sync(0xffffffffu, mx > m + (8.f + C::SHIFT))) {
-                    const float mn = fmaxf(m, mx - C::SHIFT);
-                    const float alpha = mn == -INFINITY ? 1.f : ex2(m - mn);
-                    m = mn;
-                    l *= alpha;
-                    if (t > 0) {  // s_full: the product before this step's scores is complete
+                                for (int c = 0; c < D; c += 32) {
+                                    float o[32];
+                                    tmem_ld32(t_o + c, o);
+                                    tmem_wait_ld();
 #pragma unroll
-                        for (int c = 0; c < D; c += 32) {
-                            float o[32];
-                            tmem_ld32(t_o + c, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] *= alpha;
-                            tmem_st32(t_o + c, reinterpret_cast<const uint32_t*>(o));
+                                    for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                                    tmem_st32(t_o + c, reinterpret_cast<const uint32_t*>(o));
+                                }
+                            }
                         }
                     }
+                    const float mm = m == -INFINITY ? 0.f : -m;
+                    sum = make_float2(0.f, 0.f);
+                    weights<FP8, 0, 48>(x, q2, make_float2(mm, mm), pk, sum);
+                    if (exact) break;
+                    const float mx = largest(x) * qa;
+                    if (!__any_sync(0xffffffffu, !(mx <= m + (8.f + C::SHIFT)))) break;
+                    scores();  // as they were: P has not been stored yet
                 }
-                const float mm = m == -INFINITY ? 0.f : -m;
-                const float2 q2 = make_float2(qa, qa), m2 = make_float2(mm, mm);
-                float2 sum0 = make_float2(l, 0.f), sum1 = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t pk[32];
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        float2 y = fma2(make_float2(x[64 * half + 2 * c], x[64 * half + 2 * c + 1]), q2, m2);
-                        y.x = ex2(y.x);
-                        y.y = ex2(y.y);
-                        if (c & 1) sum1 = add2(sum1, y); else sum0 = add2(sum0, y);
-                        pk[c] = FP8 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
-                    }
-                    tmem_st32(t_s + 32 * half, pk);
-                }
-                sum0 = add2(sum0, sum1);
-                l = sum0.x + sum0.y;
+                tmem_st32(t_s, pk);
+                tmem_st16(t_s + 32, pk + 32);
                 tmem_wait_st();
-                if (x_pending) {  // the item before: O of this pipeline is still being read
-                    if (!(ok = wait_warp(x_empty, x_phase))) break;
-                    x_phase ^= 1;
-                    x_pending = false;
-                }
+                if (!(ok = o_readable())) break;
                 tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[wg]);
+                arrive(C::P_FULL + 8 * wg);
+                // the last quarter of the keys, while the product of the others runs
+                const float mm = m == -INFINITY ? 0.f : -m;
+                weights<FP8, 48, 16>(x, q2, make_float2(mm, mm), pk, sum);
+                tmem_st16(t_s + 48, pk);
+                tmem_wait_st();
+                tc_fence_before();
+                arrive(C::P_REST + 8 * wg);
+                l += sum.x + sum.y;
             }
             if (!ok) break;
             base += 2 * plan.steps;
+            if (m == -INFINITY) l = 0.f;  // no key seen
             // ------------------------------------------------ end of the item
             const float vs = FP8 ? p.v_scales[u.g] : 1.f;
             const bool two = !plan.wide && plan.n1 > 0;  // both pipelines hold parts of the same rows
             float w0 = 1.f, w1 = 0.f;
             if (wg == 1 && !plan.wide) {
                 if (two) {
-                    if (x_pending) {
-                        if (!(ok = wait_warp(x_empty, x_phase))) break;
-                        x_phase ^= 1;
-                        x_pending = false;
-                    }
+                    if (!(ok = o_readable())) break;
                     ml_x[lane_row] = make_float2(m, l);
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(x_full);
+                    arrive(C::X_FULL);
                     o_phase[1] ^= 1;
                     x_pending = true;
                 }
             } else {
                 if (nt > 0) {
-                    if (!(ok = wait_warp(&o_full[wg], o_phase[wg]))) break;
+                    if (!(ok = wait(C::O_FULL + 8 * wg, o_phase[wg]))) break;
                     o_phase[wg] ^= 1;
                 }
                 if (two) {
-                    if (!(ok = wait_warp(x_full, x_phase))) break;
+                    if (!(ok = wait(C::X_FULL, x_phase))) break;
                     x_phase ^= 1;
-                    if (!(ok = wait_warp(&o_full[1], o_phase[1]))) break;
+                    if (!(ok = wait(C::O_FULL + 8, o_phase[1]))) break;
                     o_phase[1] ^= 1;
                     const float2 o = ml_x[lane_row];
                     const float M = fmaxf(m, o.x);
@@ -848,8 +985,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 if (!whole && row < rows) p.ws_ml[pr] = make_float2(m, l);
                 if (two) {  // the other pipeline's O may be written again
                     tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(x_empty);
+                    arrive(C::X_EMPTY);
                 }
                 uint32_t again = __ballot_sync(0xffffffffu, row < rows && nt > 0 && !(odd == 0.f && l == l));
                 __syncwarp();
@@ -882,23 +1018,18 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
         if constexpr (FP8) {
             regs_dec<C::REGS_WIDEN>();
             const int t128 = tid - 384;
-            int count = 0;  // loads so far
-            int q_items = 0;
+            uint32_t rs = 0, raw_phase = 0, st = 0, empty_phase = 1, q_phase = 0;
             bool ok = true;
-            for (int n = 0; ok; ++n) {
-                if (!(ok = wait_warp(&item_full[n % C::ITEMS], (n / C::ITEMS) & 1))) break;
-                const AttnItem u = *item_slot(n);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&item_empty[n % C::ITEMS]);
-                if (u.seq < 0) break;
+            AttnItem u;
+            for (int n = 0; ok && take_item(n, u); ++n) {
                 Plan plan;
                 plan.set(u, gl);
                 if (plan.steps == 0) continue;
                 const int32_t* bt = p.block_tables + (long long)u.seq * p.max_blocks_per_seq;
                 // q: bf16 -> f16 in place, each row times a power of two that brings
                 // its largest value to [2^14, 2^15)
-                if (!(ok = wait_warp(q_full, q_items & 1))) break;
-                ++q_items;
+                if (!(ok = wait(C::Q_FULL, q_phase))) break;
+                q_phase ^= 1;
                 for (int t = 0; t < (plan.wide ? 2 : 1); ++t) {
                     unsigned char* qr = smem + C::Q_OFF + t * C::QTILE + t128 * 128;
                     uint32_t top = 0;
@@ -941,9 +1072,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                         }
                 }
                 fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(q_wide);
-                for (int lo = 0; lo < 2 * plan.steps; ++lo, ++count) {
+                arrive(C::Q_WIDE);
+                for (int lo = 0; lo < 2 * plan.steps; ++lo) {
                     bool v;
                     const int k0 = u.kv0 + plan.load_step(lo, v) * C::KEYS;
                     const int key = k0 + lane * bs;
@@ -952,9 +1082,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     const bool short_step = k0 + C::KEYS > u.kv1 || bad != 0;
                     uint32_t there[4];
                     there_words(u.kv1 - k0, bad, bs, there);
-                    const int rs = count % C::NRAW, st = count % C::NSLOT;
-                    if (!(ok = wait_warp(&load_full[rs], (count / C::NRAW) & 1))) break;
-                    if (count >= C::NSLOT && !(ok = wait_warp(&slot_empty[st], (count / C::NSLOT - 1) & 1))) break;
+                    if (!(ok = wait(C::LOAD_FULL + 8 * rs, raw_phase))) break;
+                    if (!(ok = wait(C::SLOT_EMPTY + 8 * st, empty_phase))) break;
                     const unsigned char* raw = smem + C::RAW_OFF + rs * C::RAW;
                     unsigned char* wide = smem + C::SLOT_OFF + st * C::TILE;
                     constexpr int CPR = D / 16;  // 16-byte chunks of a raw row
@@ -983,11 +1112,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                         *reinterpret_cast<uint4*>(to + (((cc + 1 - first) ^ (r & 7)) << 4)) = first ? a : b;
                     }
                     fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&slot_full[st]);
-                        mbar_arrive(&load_empty[rs]);
-                    }
+                    arrive(C::SLOT_FULL + 8 * st);
+                    if (lane == 0) bar_arrive(sb + C::LOAD_EMPTY + 8 * rs);
+                    if (++rs == C::NRAW) rs = 0, raw_phase ^= 1;
+                    if (++st == C::NSLOT) st = 0, empty_phase ^= 1;
                 }
             }
         }
@@ -999,19 +1127,19 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     __syncthreads();
     if (*abort_flag) {
         // copies and products in flight land before the CTA leaves; each wait is bounded
-        auto land = [&](uint64_t* bar, uint32_t parity) {
+        auto land = [&](uint32_t off, uint32_t parity) {
             const unsigned long long t0 = globaltimer_ns();
-            while (!mbar_try_wait(bar, parity))
+            while (!bar_try(sb + off, parity))
                 if (globaltimer_ns() - t0 > kWaitTimeoutNs) break;
         };
         if (warp == 8 && lane == 0) {
             for (int li = loads > C::NLOAD ? loads - C::NLOAD : 0; li < loads; ++li)
-                land(&load_full[li % C::NLOAD], (li / C::NLOAD) & 1);
-            if (q_loads > 0) land(q_full, (q_loads - 1) & 1);
+                land(C::LOAD_FULL + 8 * (li % C::NLOAD), (li / C::NLOAD) & 1);
+            if (q_loads > 0) land(C::Q_FULL, (q_loads - 1) & 1);
         }
         if (warp == 9 && mma_any) {
-            commit_one(mma_done, elect_one());
-            land(mma_done, 0);
+            commit_one(sb + C::MMA_DONE, elect_one());
+            land(C::MMA_DONE, 0);
         }
         // parts that were not counted: empty ones, so that the counters end at zero
         AttnWalk<TcDivision> walk =
