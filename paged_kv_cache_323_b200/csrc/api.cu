@@ -499,7 +499,7 @@ int attn_impl(int kind, void* out, const void* q, const void* k_cache, const voi
     p.v_scales = v_scales;
     p.counters = reinterpret_cast<int*>(ws);
     p.ws_ml = reinterpret_cast<float2*>(ws + w.ml_off);
-    p.ws_o = reinterpret_cast<float*>(ws + w.o_off);
+    p.ws_o = reinterpret_cast<float4*>(ws + w.o_off);
     p.err = err;
     p.q_stride = q_stride;
     p.num_seqs = num_seqs;

@@ -40,7 +40,7 @@ struct AttnParams {
     const float* v_scales;
     int* counters;           // [gridDim.x] parts finished of the item whose first part the CTA owns; zero between launches
     float2* ws_ml;           // [2 gridDim.x][part_rows] (maximum in log2 units, sum)
-    float* ws_o;             // [2 gridDim.x][part_rows][D]
+    float4* ws_o;            // [2 gridDim.x][D / 4][part_rows]: neighbouring rows side by side
     int* err;
     long long q_stride;      // elements between two tokens of q
     int num_seqs;
@@ -135,7 +135,8 @@ struct AttnWalk {
             return b0 + i + (o1 < Div::FINE && o1 < K ? 1 : 0);
         }
         const int e = i + 1 < parts(at, K, share) ? (i + 1) * Div::COARSE : K;
-        return (int)((at + e - 1) / share);
+        const long long b0 = at / share;
+        return (int)b0 + (int)(((unsigned)(at - b0 * share) + (unsigned)e - 1u) / (unsigned)share);
     }
     __device__ __forceinline__ static int parts(long long at, int K, long long share) {
         if (share >= Div::COARSE) {
@@ -296,10 +297,12 @@ __device__ __forceinline__ void attn_check_parents(const AttnParams& p, const At
 }
 
 // ------------------------------------------------------------------- merge
-// First partial row of part i of an item that CTA b owns: a CTA's first item
-// may go on from the CTA before (part > 0), its last may go on in the next.
-__device__ __forceinline__ long long attn_partial_row(const AttnParams& p, int b, int part) {
-    return (long long)(2 * b + (part == 0 ? 1 : 0)) * p.part_rows;
+// Partial result of part i of an item that CTA b owns: a CTA's first item may
+// go on from the CTA before (part > 0), its last may go on in the next.
+__device__ __forceinline__ int attn_partial(int b, int part) { return 2 * b + (part == 0 ? 1 : 0); }
+// Place in ws_o of dims d .. d + 3 of a partial result's row.
+__device__ __forceinline__ long long attn_partial_at(const AttnParams& p, int partial, int D, int d, int row) {
+    return ((long long)partial * (D / 4) + d / 4) * p.part_rows + row;
 }
 
 // End of one part of a split item, called by NT threads (tid, sync() a
@@ -327,83 +330,53 @@ __device__ __forceinline__ bool attn_merge(const AttnParams& p, const AttnItem& 
     if (!sync()) return false;
     if (!*flag) return true;
     __threadfence();
-    // A warp has rows warp, warp + NT / 32, ..: lane k looks after the maxima and sums
-    // of the k-th of them, then the warp adds up RB rows x PB parts at a time, so that
-    // many loads are in flight whether the rows are many or the parts.
-    constexpr int NW = NT / 32, VE = D / 32, RB = 4, PB = 4;
-    static_assert(Div::ROWS <= 32 * NW, "a lane per row");
-    const int warp = tid >> 5, lane = tid & 31;
-    const int mine = warp + NW * lane;
-    float M = -INFINITY, L = 0.f;
-    if (mine < rows) {
-#pragma unroll 4
-        for (int i = 0; i < it.nparts; ++i)
-            M = fmaxf(M, __ldcg(&p.ws_ml[attn_partial_row(p, Walk::owner(it.at, it.keys, share, i), i) + mine]).x);
-#pragma unroll 4
+    // a thread takes 16 dims of a row; threads side by side take neighbouring rows
+    const int units = rows * (D / 16);
+    for (int unit = tid; unit < units; unit += NT) {
+        const int c = unit / rows, r = unit - c * rows;
+        float M = -INFINITY, L = 0.f, acc[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+#pragma unroll 2
         for (int i = 0; i < it.nparts; ++i) {
-            const float2 ml = __ldcg(&p.ws_ml[attn_partial_row(p, Walk::owner(it.at, it.keys, share, i), i) + mine]);
-            // no key seen in any part: all sums are 0 (or NaN), taken as they are
-            L = fmaf(M == -INFINITY ? 1.f : exp2f(ml.x - M), ml.y, L);
-        }
-    }
-    const float inv = L == 0.f ? 0.f : 1.f / L;  // no key seen: a zero row
-    for (int k0 = 0; warp + NW * k0 < rows; k0 += RB) {
-        float acc[RB][VE];
+            const int slot = attn_partial(Walk::owner(it.at, it.keys, share, i), i);
+            const float2 ml = __ldcg(&p.ws_ml[(long long)slot * p.part_rows + r]);
+            const float4* o = p.ws_o + attn_partial_at(p, slot, D, 16 * c, r);
+            float4 v[4];
 #pragma unroll
-        for (int j = 0; j < RB; ++j)
+            for (int e = 0; e < 4; ++e) v[e] = __ldcg(o + e * (long long)p.part_rows);
+            const float Mn = fmaxf(M, ml.x);
+            // no key seen in any part so far: the sums are 0 (or NaN), taken as they are
+            const float a = Mn == -INFINITY ? 1.f : exp2f(M - Mn), w = Mn == -INFINITY ? 1.f : exp2f(ml.x - Mn);
+            M = Mn;
+            L = fmaf(w, ml.y, L * a);
 #pragma unroll
-            for (int e = 0; e < VE; ++e) acc[j][e] = 0.f;
-        for (int i0 = 0; i0 < it.nparts; i0 += PB) {
-            float w[PB], v[PB][RB][VE];
-#pragma unroll
-            for (int b = 0; b < PB; ++b) {
-                const int i = i0 + b;
-                const bool there = i < it.nparts;
-                const long long base = there ? attn_partial_row(p, Walk::owner(it.at, it.keys, share, i), i) : 0;
-                w[b] = 0.f;
-                if (there && mine < rows) {
-                    const float m = __ldcg(&p.ws_ml[base + mine]).x;
-                    w[b] = (M == -INFINITY ? 1.f : exp2f(m - M)) * inv;
-                }
-#pragma unroll
-                for (int j = 0; j < RB; ++j) {
-                    const int r = warp + NW * (k0 + j);
-                    const float* o = p.ws_o + (base + r) * D + lane * VE;
-                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (there && r < rows) {
-                        if constexpr (VE == 4) {
-                            x = __ldcg(reinterpret_cast<const float4*>(o));
-                        } else {
-                            const float2 y = __ldcg(reinterpret_cast<const float2*>(o));
-                            x = make_float4(y.x, y.y, 0.f, 0.f);
-                        }
-                    }
-                    v[b][j][0] = x.x;
-                    v[b][j][1] = x.y;
-                    if constexpr (VE == 4) {
-                        v[b][j][2] = x.z;
-                        v[b][j][3] = x.w;
-                    }
-                }
+            for (int e = 0; e < 4; ++e) {
+                acc[4 * e] = fmaf(w, v[e].x, acc[4 * e] * a);
+                acc[4 * e + 1] = fmaf(w, v[e].y, acc[4 * e + 1] * a);
+                acc[4 * e + 2] = fmaf(w, v[e].z, acc[4 * e + 2] * a);
+                acc[4 * e + 3] = fmaf(w, v[e].w, acc[4 * e + 3] * a);
             }
-#pragma unroll
-            for (int b = 0; b < PB; ++b)
-#pragma unroll
-                for (int j = 0; j < RB; ++j) {
-                    const float wj = __shfl_sync(0xffffffffu, w[b], k0 + j);
-#pragma unroll
-                    for (int e = 0; e < VE; ++e) acc[j][e] = fmaf(wj, v[b][j][e], acc[j][e]);
-                }
         }
+        const float inv = L == 0.f ? 0.f : 1.f / L;  // no key seen: a zero row
+        T* dst = static_cast<T*>(p.out) +
+                 ((long long)(it.row + (r >> p.group_log2)) * p.num_heads + it.g * G + (r & (G - 1))) * D + 16 * c;
+        if constexpr (sizeof(T) == 2) {
 #pragma unroll
-        for (int j = 0; j < RB; ++j) {
-            const int r = warp + NW * (k0 + j);
-            if (r >= rows) continue;
-            T* dst = static_cast<T*>(p.out) +
-                     ((long long)(it.row + (r >> p.group_log2)) * p.num_heads + it.g * G + (r & (G - 1))) * D +
-                     lane * VE;
+            for (int h = 0; h < 2; ++h) {
+                uint32_t w[4];
 #pragma unroll
-            for (int e = 0; e < VE; ++e) Elem<T>::store(dst + e, acc[j][e]);
+                for (int e = 0; e < 4; ++e) {
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(acc[8 * h + 2 * e] * inv, acc[8 * h + 2 * e + 1] * inv);
+                    w[e] = *reinterpret_cast<const uint32_t*>(&b);
+                }
+                reinterpret_cast<uint4*>(dst)[h] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                reinterpret_cast<float4*>(dst)[e] = make_float4(acc[4 * e] * inv, acc[4 * e + 1] * inv,
+                                                                acc[4 * e + 2] * inv, acc[4 * e + 3] * inv);
         }
     }
     return true;

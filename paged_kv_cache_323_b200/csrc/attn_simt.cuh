@@ -220,13 +220,12 @@ __global__ void __launch_bounds__(256, 2) attn_simt_kernel(const AttnParams p) {
                     *reinterpret_cast<float4*>(dst + 64 * j + 4 * tx) = make_float4(
                         o[i][4 * j] * inv, o[i][4 * j + 1] * inv, o[i][4 * j + 2] * inv, o[i][4 * j + 3] * inv);
             } else {
-                const long long pr = attn_partial_row(p, blockIdx.x, u.part) + r;
-                if (tx == 0) p.ws_ml[pr] = make_float2(m[i], l[i]);
+                const int slot = attn_partial(blockIdx.x, u.part);
+                if (tx == 0) p.ws_ml[(long long)slot * p.part_rows + r] = make_float2(m[i], l[i]);
 #pragma unroll
                 for (int j = 0; j < OJ; ++j)
-                    *reinterpret_cast<float4*>(p.ws_o + pr * D + 64 * j + 4 * tx) =
-                        make_float4(o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2],
-                                    o[i][4 * j + 3]);
+                    p.ws_o[attn_partial_at(p, slot, D, 64 * j + 4 * tx, r)] =
+                        make_float4(o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]);
             }
         }
         if (u.nparts > 1)

@@ -16,10 +16,11 @@
 //              TMEM, over the columns of S it came from),
 //     O += P V (P from TMEM, V from shared memory, O in TMEM),
 // and while one is in its softmax the tensor cores work for the other.  O
-// stays in TMEM for the whole item: it is scaled down only when a row's
-// maximum has grown by more than 2^8 since the last time (a stale maximum
-// cancels in the quotient; P stays below 2^8), which after the first steps
-// hardly ever happens.
+// stays in TMEM for the whole item and the maximum that the weights are taken
+// by is allowed to be an old one, which cancels in the quotient: with bf16
+// weights it is renewed, and O scaled, after a step that exceeds it by 2^40,
+// with f16 ones before a step that exceeds it by 2^8; either hardly ever
+// happens once an item has begun, and the new maximum is found on the side.
 //
 // Warps: 0-3 and 4-7 softmax, 8 producer (TMA: one 5-D copy brings a whole
 // block of K or V in the layout the MMA wants), 9 MMA issue, 10 the walk;
@@ -249,16 +250,15 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return r;
 }
 
-// Weights 2^(x q + m) of the pairs [C0, C0 + CN) of a row's scores, packed for
-// the MMA; sum gets their total.  One pair in POLY_OF goes by ex2_poly, so that
-// the special-function unit (a quarter of the lanes a clock) and the FMA pipe
-// share the work.
+// Weights 2^(x q + m) of 32 scores of a row, packed for the MMA; sum gets their
+// total.  One pair in POLY_OF goes by ex2_poly, so that the special-function
+// unit (a quarter of the lanes a clock) and the FMA pipe share the work.
 constexpr int POLY_OF = 4;
-template <bool FP8, int C0, int CN>
-__device__ __forceinline__ void weights(const float* x, float2 q, float2 m, uint32_t* pk, float2& sum) {
+template <bool FP8>
+__device__ __forceinline__ void weights32(const float* x, float2 q, float2 m, uint32_t* pk, float2& sum) {
     float2 sum1 = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int c = C0; c < C0 + CN; ++c) {
+    for (int c = 0; c < 16; ++c) {
         float2 y = fma2(make_float2(x[2 * c], x[2 * c + 1]), q, m);
         if (c % POLY_OF == POLY_OF - 1) {
             y = ex2_poly(y);
@@ -267,24 +267,21 @@ __device__ __forceinline__ void weights(const float* x, float2 q, float2 m, uint
             y.y = ex2(y.y);
         }
         if (c & 1) sum1 = add2(sum1, y); else sum = add2(sum, y);
-        pk[c - C0] = FP8 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
+        pk[c] = FP8 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
     }
     sum = add2(sum, sum1);
 }
 
-// Largest of a row's scores; NaN if any of them is.
-__device__ __forceinline__ float largest(const float* x) {
-    float m0 = x[0], m1 = x[1], m2 = x[2], m3 = x[3];
+// Largest of m and 32 scores; NaN if any of them is.
+__device__ __forceinline__ float largest32(const float* x, float m) {
+    float m0 = max3_nan(m, x[0], x[1]), m1 = max3_nan(x[2], x[3], x[4]);
 #pragma unroll
-    for (int c = 4; c < 124; c += 8) {
+    for (int c = 5; c < 29; c += 4) {
         m0 = max3_nan(m0, x[c], x[c + 1]);
         m1 = max3_nan(m1, x[c + 2], x[c + 3]);
-        m2 = max3_nan(m2, x[c + 4], x[c + 5]);
-        m3 = max3_nan(m3, x[c + 6], x[c + 7]);
     }
-    m0 = max3_nan(m0, x[124], x[125]);
-    m1 = max3_nan(m1, x[126], x[127]);
-    return max3_nan(max3_nan(m0, m1, m2), m3, m3);
+    m0 = max3_nan(m0, x[29], x[30]);
+    return max3_nan(m0, m1, x[31]);
 }
 
 // ---------------------------------------------------------------- geometry
@@ -314,9 +311,9 @@ struct Cfg {
     static constexpr int REGS_LAUNCH = 65536 / THREADS / 8 * 8;
     static_assert(256 * REGS_SOFTMAX + 128 * REGS_ISSUE + (FP8 ? 128 * REGS_WIDEN : 0) <= THREADS * REGS_LAUNCH,
                   "the roles' registers come out of the launch's");
-    // P is held 2^SHIFT times larger where it is f16, whose smallest step is 2^-24: its
-    // largest value then stays below 2^15, and a weight loses less than 2^-32 of the largest
-    static constexpr float SHIFT = FP8 ? 7.f : 0.f;
+    // f16 weights are held 2^7 times larger: below 2^15, and a weight loses less than
+    // 2^-32 of the largest to f16's smallest step, 2^-24
+    static constexpr float SHIFT = 7.f;
     static constexpr uint32_t TMEM_COLS = 512;      // S / P of both pipelines, then O of both
     static constexpr uint32_t O_COL = 256;
     static constexpr uint32_t FORMAT = FP8 ? 0u : 1u;  // f16 or bf16
@@ -805,6 +802,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             const int row0 = (plan.wide ? wg * 128 : 0) + (warp & 3) * 32;
             const int clear = par ? u.first : u.pos + (row0 >> gl) + 1;
             float m = -INFINITY, l = 0.f;
+            float alpha_next = 1.f;  // what O is to be scaled by before the next product
+            bool stale = false;
             auto entry = [&](int t) {  // lane j: whether block j of step t is not in the pool
                 const int key = u.kv0 + plan.step(wg, t) * C::KEYS + lane * bs;
                 if (t >= nt || lane >= bpt || key >= u.kv1) return 0;
@@ -818,23 +817,15 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 if (!(ok = wait(C::S_FULL + 8 * wg, s_phase))) break;
                 s_phase ^= 1;
                 tc_fence_after();
-                float x[128];
-                auto scores = [&]() {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, x + 32 * c);
-                    tmem_wait_ld();
-                };
-                scores();
                 const bool short_step = k0 + C::KEYS > u.kv1 || bad != 0;
                 const bool masked = short_step || k0 + C::KEYS > clear;
+                uint32_t w[4];
                 if (masked) {
-                    uint32_t w[4], there[4];
+                    uint32_t there[4];
                     seen_words(par, u.first, qi, k0, w);
                     there_words(u.kv1 - k0, bad, bs, there);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) w[c] &= there[c];
-#pragma unroll
-                    for (int c = 0; c < 128; ++c) x[c] = w[c >> 5] & (1u << (c & 31)) ? x[c] : -INFINITY;
                     if (!FP8 && short_step && (!plan.wide || wg == 0 || j >= plan.n0)) {
                         // keys that are not there: their rows of V may hold anything
                         const int li = base + plan.v_load(j), st = li % C::NSLOT;
@@ -853,56 +844,96 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                         fence_proxy_async_smem();
                     }
                 }
-                uint32_t pk[48];
-                float2 sum;
-                // The old maximum does for a step that does not exceed it by more than 2^8,
-                // as hardly any does once an item has begun: the weights are taken with it
-                // while the new one is still being found, and are taken again if it does not.
-                for (bool exact = masked || t == 0;; exact = true) {
-                    if (exact) {
-                        float mx = largest(x) * qa;
-                        if (__any_sync(0xffffffffu, !(mx <= m + (8.f + C::SHIFT)))) {
-                            // a score that is NaN or infinite: a row of NaN, for slow_row
-                            if (!(mx < INFINITY)) mx = __uint_as_float(0x7fffffffu);
-                            const float mn = mx - C::SHIFT > m || mx != mx ? mx - C::SHIFT : m;
-                            const float alpha = mn == -INFINITY ? 1.f : ex2(m - mn);
-                            m = mn;
-                            l *= alpha;
-                            if (t > 0) {  // s_full: the product before this step's scores is complete
+                auto mask32 = [&](float* x, int c) {
+                    const uint32_t word = c == 0 ? w[0] : c == 1 ? w[1] : c == 2 ? w[2] : w[3];
 #pragma unroll
-                                for (int c = 0; c < D; c += 32) {
-                                    float o[32];
-                                    tmem_ld32(t_o + c, o);
-                                    tmem_wait_ld();
+                    for (int e = 0; e < 32; ++e) x[e] = word & (1u << e) ? x[e] : -INFINITY;
+                };
+                auto rescale_o = [&](float alpha) {  // s_full: the product before this step's scores is complete
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        float o[32];
+                        tmem_ld32(t_o + c, o);
+                        tmem_wait_ld();
 #pragma unroll
-                                    for (int e = 0; e < 32; ++e) o[e] *= alpha;
-                                    tmem_st32(t_o + c, reinterpret_cast<const uint32_t*>(o));
-                                }
-                            }
-                        }
+                        for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                        tmem_st32(t_o + c, reinterpret_cast<const uint32_t*>(o));
+                    }
+                };
+                // 32 keys at a time, the next ones on their way: a loop, because straight
+                // code for all 128 runs at the pace of the instruction fetch
+                float xa[32], xb[32], mx = -INFINITY;
+                if constexpr (FP8) {
+                    // f16 weights: the maximum first
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_ld32(t_s + 32 * c, xa);
+                        tmem_wait_ld();
+                        if (masked) mask32(xa, c);
+                        mx = largest32(xa, mx);
+                    }
+                    mx *= qa;
+                    if (__any_sync(0xffffffffu, !(mx <= m + (8.f + C::SHIFT)))) {
+                        if (!(mx < INFINITY)) l = __uint_as_float(0x7fffffffu);  // for slow_row
+                        const float mn = fmaxf(m, mx - C::SHIFT);
+                        const float alpha = mn == -INFINITY ? 1.f : ex2(m - mn);
+                        m = mn;
+                        l *= alpha;
+                        if (t > 0) rescale_o(alpha);
+                    }
+                } else if (stale) {
+                    rescale_o(alpha_next);
+                    stale = false;
+                }
+                float2 sum = make_float2(0.f, 0.f);
+                auto chunk = [&](float* x, int c) {
+                    if (masked) mask32(x, c);
+                    uint32_t pk[16];
+                    if constexpr (!FP8) {
+                        mx = largest32(x, mx);
+                        // the first keys that a row sees give its maximum for now
+                        if (masked || t == 0) m = m == -INFINITY ? mx * qa : m;
                     }
                     const float mm = m == -INFINITY ? 0.f : -m;
-                    sum = make_float2(0.f, 0.f);
-                    weights<FP8, 0, 48>(x, q2, make_float2(mm, mm), pk, sum);
-                    if (exact) break;
-                    const float mx = largest(x) * qa;
-                    if (!__any_sync(0xffffffffu, !(mx <= m + (8.f + C::SHIFT)))) break;
-                    scores();  // as they were: P has not been stored yet
+                    weights32<FP8>(x, q2, make_float2(mm, mm), pk, sum);
+                    tmem_st16(t_s + 16 * c, pk);  // over scores that have been read
+                };
+                tmem_ld32(t_s, xa);
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    tmem_wait_ld();
+                    tmem_ld32(t_s + 64 * h + 32, xb);
+                    chunk(xa, 2 * h);
+                    tmem_wait_ld();
+                    if (h == 0) {
+                        tmem_ld32(t_s + 64, xa);
+                    } else {  // the product of the first 96 keys may start
+                        tmem_wait_st();
+                        if (!(ok = o_readable())) break;
+                        tc_fence_before();
+                        arrive(C::P_FULL + 8 * wg);
+                    }
+                    chunk(xb, 2 * h + 1);
                 }
-                tmem_st32(t_s, pk);
-                tmem_st16(t_s + 32, pk + 32);
-                tmem_wait_st();
-                if (!(ok = o_readable())) break;
-                tc_fence_before();
-                arrive(C::P_FULL + 8 * wg);
-                // the last quarter of the keys, while the product of the others runs
-                const float mm = m == -INFINITY ? 0.f : -m;
-                weights<FP8, 48, 16>(x, q2, make_float2(mm, mm), pk, sum);
-                tmem_st16(t_s + 48, pk);
+                if (!ok) break;
                 tmem_wait_st();
                 tc_fence_before();
                 arrive(C::P_REST + 8 * wg);
                 l += sum.x + sum.y;
+                if constexpr (!FP8) {
+                    mx *= qa;
+                    if (__any_sync(0xffffffffu, !(mx <= m + 40.f))) {
+                        // NaN, infinite, or past what ex2_poly takes: for slow_row
+                        if (!(mx <= m + 120.f) && mx != -INFINITY) l = __uint_as_float(0x7fffffffu);
+                        if (t + 1 < nt) {
+                            const float mn = mx > m ? mx : m;
+                            alpha_next = mn == -INFINITY ? 1.f : ex2(m - mn);
+                            m = mn;
+                            l *= alpha_next;
+                            stale = true;  // O: once this step's product is complete
+                        }
+                    }
+                }
             }
             if (!ok) break;
             base += 2 * plan.steps;
@@ -945,9 +976,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 w1 *= inv;
                 __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
                                      ((long long)(u.row + (row >> gl)) * p.num_heads + u.g * G + (row & (G - 1))) * D;
-                const long long pr = attn_partial_row(p, blockIdx.x, u.part) + row;
+                const int slot = attn_partial(blockIdx.x, u.part);
                 float odd = 0.f;  // becomes NaN with the first value that is not finite
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     float o[32];
 #pragma unroll
@@ -977,12 +1008,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                         } else {
 #pragma unroll
                             for (int e = 0; e < 32; e += 4)
-                                *reinterpret_cast<float4*>(p.ws_o + pr * D + c + e) =
+                                p.ws_o[attn_partial_at(p, slot, D, c + e, row)] =
                                     make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                         }
                     }
                 }
-                if (!whole && row < rows) p.ws_ml[pr] = make_float2(m, l);
+                if (!whole && row < rows) p.ws_ml[(long long)slot * p.part_rows + row] = make_float2(m, l);
                 if (two) {  // the other pipeline's O may be written again
                     tc_fence_before();
                     arrive(C::X_EMPTY);
@@ -994,7 +1025,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     again &= again - 1;
                     float ms, ls, acc[D / 32];
                     slow_row<D, FP8>(p, u, row0 + r, ms, ls, acc);
-                    const long long at = __shfl_sync(0xffffffffu, pr, r);
                     const int rr = row0 + r;
                     __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) +
                                         ((long long)(u.row + (rr >> gl)) * p.num_heads + u.g * G + (rr & (G - 1))) * D;
@@ -1003,9 +1033,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                         if (whole)
                             to[lane * (D / 32) + e] = __float2bfloat16_rn(ls == 0.f ? 0.f : acc[e] / ls);
                         else
-                            p.ws_o[at * D + lane * (D / 32) + e] = acc[e];
+                            reinterpret_cast<float*>(p.ws_o + attn_partial_at(p, slot, D, lane * (D / 32), rr))
+                                [(lane * (D / 32)) % 4 + e] = acc[e];
                     }
-                    if (!whole && lane == 0) p.ws_ml[at] = make_float2(ms, ls);
+                    if (!whole && lane == 0) p.ws_ml[(long long)slot * p.part_rows + rr] = make_float2(ms, ls);
                 }
             }
             if (u.nparts > 1) {
@@ -1150,7 +1181,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             while (walk.next(p, u)) {
                 if (u.nparts == 1 || k++ < *turns) continue;
                 for (int r = 0; r < (u.ntok << gl); ++r)
-                    p.ws_ml[attn_partial_row(p, blockIdx.x, u.part) + r] = make_float2(-INFINITY, 0.f);
+                    p.ws_ml[(long long)attn_partial(blockIdx.x, u.part) * p.part_rows + r] = make_float2(-INFINITY, 0.f);
                 __threadfence();
                 int* c = p.counters + AttnWalk<TcDivision>::owner(u.at, u.keys, walk.share, 0);
                 if (atomicAdd(c, 1) == u.nparts - 1) *c = 0;
