@@ -337,25 +337,43 @@ __device__ __forceinline__ bool attn_merge(const AttnParams& p, const AttnItem& 
         float M = -INFINITY, L = 0.f, acc[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-#pragma unroll 2
-        for (int i = 0; i < it.nparts; ++i) {
-            const int slot = attn_partial(Walk::owner(it.at, it.keys, share, i), i);
-            const float2 ml = __ldcg(&p.ws_ml[(long long)slot * p.part_rows + r]);
-            const float4* o = p.ws_o + attn_partial_at(p, slot, D, 16 * c, r);
-            float4 v[4];
+        for (int i0 = 0; i0 < it.nparts; i0 += 2) {
+            float2 ml[2];
+            float4 v[2][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = __ldcg(o + e * (long long)p.part_rows);
-            const float Mn = fmaxf(M, ml.x);
+            for (int b = 0; b < 2; ++b) {
+                const int i = i0 + b;
+                ml[b] = make_float2(-INFINITY, 0.f);
+                if (i < it.nparts) {
+                    const int slot = attn_partial(Walk::owner(it.at, it.keys, share, i), i);
+                    ml[b] = __ldcg(&p.ws_ml[(long long)slot * p.part_rows + r]);
+                    const float4* o = p.ws_o + attn_partial_at(p, slot, D, 16 * c, r);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[b][e] = __ldcg(o + e * (long long)p.part_rows);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[b][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+            }
+            const float Mn = fmaxf(M, fmaxf(ml[0].x, ml[1].x));
             // no key seen in any part so far: the sums are 0 (or NaN), taken as they are
-            const float a = Mn == -INFINITY ? 1.f : exp2f(M - Mn), w = Mn == -INFINITY ? 1.f : exp2f(ml.x - Mn);
+            const bool none = Mn == -INFINITY;
+            const float a = none ? 1.f : exp2f(M - Mn);
             M = Mn;
-            L = fmaf(w, ml.y, L * a);
+            L *= a;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                acc[4 * e] = fmaf(w, v[e].x, acc[4 * e] * a);
-                acc[4 * e + 1] = fmaf(w, v[e].y, acc[4 * e + 1] * a);
-                acc[4 * e + 2] = fmaf(w, v[e].z, acc[4 * e + 2] * a);
-                acc[4 * e + 3] = fmaf(w, v[e].w, acc[4 * e + 3] * a);
+            for (int e = 0; e < 16; ++e) acc[e] *= a;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const float w = none ? 1.f : exp2f(ml[b].x - Mn);
+                L = fmaf(w, ml[b].y, L);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    acc[4 * e] = fmaf(w, v[b][e].x, acc[4 * e]);
+                    acc[4 * e + 1] = fmaf(w, v[b][e].y, acc[4 * e + 1]);
+                    acc[4 * e + 2] = fmaf(w, v[b][e].z, acc[4 * e + 2]);
+                    acc[4 * e + 3] = fmaf(w, v[b][e].w, acc[4 * e + 3]);
+                }
             }
         }
         const float inv = L == 0.f ? 0.f : 1.f / L;  // no key seen: a zero row

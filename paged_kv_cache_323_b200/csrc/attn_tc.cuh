@@ -16,11 +16,14 @@
 //              TMEM, over the columns of S it came from),
 //     O += P V (P from TMEM, V from shared memory, O in TMEM),
 // and while one is in its softmax the tensor cores work for the other.  O
-// stays in TMEM for the whole item and the maximum that the weights are taken
-// by is allowed to be an old one, which cancels in the quotient: with bf16
-// weights it is renewed, and O scaled, after a step that exceeds it by 2^40,
-// with f16 ones before a step that exceeds it by 2^8; either hardly ever
-// happens once an item has begun, and the new maximum is found on the side.
+// stays in TMEM for the whole item.
+//
+// The reference m of a row's weights need not be its maximum, it cancels in
+// the quotient.  With bf16 weights, as wide in range as fp32, m is the largest
+// of the first 32 scores that the row sees, and no other maximum is taken: when
+// the sum has passed 2^40 after a step, m, the sum and O are moved by its
+// power of two (hardly ever).  f16 weights (fp8 caches) take the maximum of a
+// step first and move m when it is exceeded by 2^8.
 //
 // Warps: 0-3 and 4-7 softmax, 8 producer (TMA: one 5-D copy brings a whole
 // block of K or V in the layout the MMA wants), 9 MMA issue, 10 the walk;
@@ -37,6 +40,8 @@
 #pragma once
 
 #include <cuda.h>
+
+#include <type_traits>
 
 #include "attn_common.cuh"
 #include "decode_tc.cuh"
@@ -221,11 +226,13 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
     return d;
 }
 
-// 2^x of two values up to 127 (0 below -125) on the FMA pipe: x = n + f with n
-// the nearest integer and |f| <= 1/2, 2^f by the polynomial of degree 3 with
-// the least relative error there (an exchange algorithm's; 7.5e-5, a thirtieth
-// of bf16's half step), n added to the exponent.  Not for NaN.
+// 2^x of two values on the FMA pipe: x = n + f with n the nearest integer and
+// |f| <= 1/2, 2^f by the polynomial of degree 3 with the least relative error
+// there (an exchange algorithm's; 7.5e-5, a thirtieth of bf16's half step), n
+// added to the exponent.  Below -125 it gives 2^-125, above 127 and for NaN 2^127.
 __device__ __forceinline__ float2 ex2_poly(float2 x) {
+    x.x = fmaxf(fminf(x.x, 127.f), -125.f);
+    x.y = fmaxf(fminf(x.y, 127.f), -125.f);
     const float2 big = make_float2(12582912.f, 12582912.f), neg = make_float2(-12582912.f, -12582912.f);
     const float2 t = add2(x, big);  // 1.5 2^23 + n: n in the low bits
     const float2 n = add2(t, neg);
@@ -234,8 +241,8 @@ __device__ __forceinline__ float2 ex2_poly(float2 x) {
                     make_float2(0.2426111251115799f, 0.2426111251115799f));
     y = fma2(y, f, make_float2(0.6932609677314758f, 0.6932609677314758f));
     y = fma2(y, f, make_float2(0.9999280571937561f, 0.9999280571937561f));
-    y.x = x.x < -125.f ? 0.f : __uint_as_float(__float_as_uint(y.x) + (__float_as_uint(t.x) << 23));
-    y.y = x.y < -125.f ? 0.f : __uint_as_float(__float_as_uint(y.y) + (__float_as_uint(t.y) << 23));
+    y.x = __uint_as_float(__float_as_uint(y.x) + (__float_as_uint(t.x) << 23));
+    y.y = __uint_as_float(__float_as_uint(y.y) + (__float_as_uint(t.y) << 23));
     return y;
 }
 
@@ -250,15 +257,15 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return r;
 }
 
-// Weights 2^(x q + m) of 32 scores of a row, packed for the MMA; sum gets their
+// Weights 2^(x q + m) of N scores of a row, packed for the MMA; sum gets their
 // total.  One pair in POLY_OF goes by ex2_poly, so that the special-function
 // unit (a quarter of the lanes a clock) and the FMA pipe share the work.
-constexpr int POLY_OF = 4;
-template <bool FP8>
-__device__ __forceinline__ void weights32(const float* x, float2 q, float2 m, uint32_t* pk, float2& sum) {
+constexpr int POLY_OF = 8;
+template <bool FP8, int N>
+__device__ __forceinline__ void weights(const float* x, float2 q, float2 m, uint32_t* pk, float2& sum) {
     float2 sum1 = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
+    for (int c = 0; c < N / 2; ++c) {
         float2 y = fma2(make_float2(x[2 * c], x[2 * c + 1]), q, m);
         if (c % POLY_OF == POLY_OF - 1) {
             y = ex2_poly(y);
@@ -844,11 +851,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                         fence_proxy_async_smem();
                     }
                 }
-                auto mask32 = [&](float* x, int c) {
-                    const uint32_t word = c == 0 ? w[0] : c == 1 ? w[1] : c == 2 ? w[2] : w[3];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) x[e] = word & (1u << e) ? x[e] : -INFINITY;
-                };
                 auto rescale_o = [&](float alpha) {  // s_full: the product before this step's scores is complete
 #pragma unroll 1
                     for (int c = 0; c < D; c += 32) {
@@ -860,17 +862,20 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                         tmem_st32(t_o + c, reinterpret_cast<const uint32_t*>(o));
                     }
                 };
-                // 32 keys at a time, the next ones on their way: a loop, because straight
-                // code for all 128 runs at the pace of the instruction fetch
-                float xa[32], xb[32], mx = -INFINITY;
+                auto mask32 = [&](float* x, uint32_t word) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e] = word & (1u << e) ? x[e] : -INFINITY;
+                };
                 if constexpr (FP8) {
                     // f16 weights: the maximum first
+                    float mx = -INFINITY;
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
-                        tmem_ld32(t_s + 32 * c, xa);
+                        float x[32];
+                        tmem_ld32(t_s + 32 * c, x);
                         tmem_wait_ld();
-                        if (masked) mask32(xa, c);
-                        mx = largest32(xa, mx);
+                        if (__builtin_expect(masked, 0)) mask32(x, c == 0 ? w[0] : c == 1 ? w[1] : c == 2 ? w[2] : w[3]);
+                        mx = largest32(x, mx);
                     }
                     mx *= qa;
                     if (__any_sync(0xffffffffu, !(mx <= m + (8.f + C::SHIFT)))) {
@@ -886,34 +891,51 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     stale = false;
                 }
                 float2 sum = make_float2(0.f, 0.f);
-                auto chunk = [&](float* x, int c) {
-                    if (masked) mask32(x, c);
-                    uint32_t pk[16];
-                    if constexpr (!FP8) {
-                        mx = largest32(x, mx);
-                        // the first keys that a row sees give its maximum for now
-                        if (masked || t == 0) m = m == -INFINITY ? mx * qa : m;
-                    }
-                    const float mm = m == -INFINITY ? 0.f : -m;
-                    weights32<FP8>(x, q2, make_float2(mm, mm), pk, sum);
-                    tmem_st16(t_s + 16 * c, pk);  // over scores that have been read
-                };
-                tmem_ld32(t_s, xa);
+                if (masked || t == 0 || __any_sync(0xffffffffu, m == -INFINITY)) {
+                    // steps with masks or without a reference, in a short loop
 #pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    tmem_wait_ld();
-                    tmem_ld32(t_s + 64 * h + 32, xb);
-                    chunk(xa, 2 * h);
-                    tmem_wait_ld();
-                    if (h == 0) {
-                        tmem_ld32(t_s + 64, xa);
-                    } else {  // the product of the first 96 keys may start
-                        tmem_wait_st();
-                        if (!(ok = o_readable())) break;
-                        tc_fence_before();
-                        arrive(C::P_FULL + 8 * wg);
+                    for (int c = 0; c < 4; ++c) {
+                        float x[32];
+                        uint32_t pk[16];
+                        tmem_ld32(t_s + 32 * c, x);
+                        tmem_wait_ld();
+                        const uint32_t word = !masked ? 0xffffffffu : c == 0 ? w[0] : c == 1 ? w[1] : c == 2 ? w[2] : w[3];
+                        mask32(x, word);
+                        // the first keys that a row sees give its reference
+                        if (!FP8 && __any_sync(0xffffffffu, m == -INFINITY)) {
+                            const float mx = largest32(x, -INFINITY) * qa;
+                            m = m == -INFINITY ? mx : m;
+                        }
+                        const float mm = m == -INFINITY ? 0.f : -m;
+                        weights<FP8, 32>(x, q2, make_float2(mm, mm), pk, sum);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)  // no weight at all, not 2^-125
+                            pk[e] &= (word & (1u << 2 * e) ? 0xffffu : 0u) | (word & (2u << 2 * e) ? 0xffff0000u : 0u);
+                        tmem_st16(t_s + 16 * c, pk);  // over scores that have been read
+                        if (c == 2) {
+                            tmem_wait_st();
+                            if (!(ok = o_readable())) break;
+                            tc_fence_before();
+                            arrive(C::P_FULL + 8 * wg);
+                        }
                     }
-                    chunk(xb, 2 * h + 1);
+                } else {
+                    float x[128];
+                    uint32_t pk[48];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, x + 32 * c);
+                    tmem_wait_ld();
+                    const float2 m2 = make_float2(-m, -m);
+                    weights<FP8, 96>(x, q2, m2, pk, sum);
+                    tmem_st32(t_s, pk);
+                    tmem_st16(t_s + 32, pk + 32);
+                    tmem_wait_st();
+                    // the product of the first 96 keys may start (a step that is not the
+                    // item's first: o_readable has been asked)
+                    tc_fence_before();
+                    arrive(C::P_FULL + 8 * wg);
+                    weights<FP8, 32>(x + 96, q2, m2, pk, sum);
+                    tmem_st16(t_s + 48, pk);
                 }
                 if (!ok) break;
                 tmem_wait_st();
@@ -921,14 +943,13 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 arrive(C::P_REST + 8 * wg);
                 l += sum.x + sum.y;
                 if constexpr (!FP8) {
-                    mx *= qa;
-                    if (__any_sync(0xffffffffu, !(mx <= m + 40.f))) {
-                        // NaN, infinite, or past what ex2_poly takes: for slow_row
-                        if (!(mx <= m + 120.f) && mx != -INFINITY) l = __uint_as_float(0x7fffffffu);
+                    if (__any_sync(0xffffffffu, !(l <= 0x1p40f))) {
+                        // NaN, infinite, or past what a weight can hold: for slow_row
+                        if (!(l <= 0x1p100f)) l = __uint_as_float(0x7fffffffu);
                         if (t + 1 < nt) {
-                            const float mn = mx > m ? mx : m;
-                            alpha_next = mn == -INFINITY ? 1.f : ex2(m - mn);
-                            m = mn;
+                            const uint32_t e = l > 1.f ? (__float_as_uint(l) >> 23) - 127 : 0;  // l in [2^e, 2^(e + 1))
+                            alpha_next = __uint_as_float((127 - e) << 23);
+                            m += (float)e;
                             l *= alpha_next;
                             stale = true;  // O: once this step's product is complete
                         }
@@ -977,27 +998,30 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
                                      ((long long)(u.row + (row >> gl)) * p.num_heads + u.g * G + (row & (G - 1))) * D;
                 const int slot = attn_partial(blockIdx.x, u.part);
-                float odd = 0.f;  // becomes NaN with the first value that is not finite
+                float2 odd = make_float2(0.f, 0.f);  // becomes NaN with the first value that is not finite
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     float o[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = 0.f;
                     if (nt > 0) {
                         tmem_ld32(t_o + c, o);
-                        tmem_wait_ld();
+                        if (two) {
+                            float o1[32];
+                            tmem_ld32(t_lane + C::O_COL + 128 + c, o1);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] *= w0;
+                            for (int e = 0; e < 32; ++e) o[e] = fmaf(o1[e], w1, o[e] * w0);
+                        } else {
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] *= w0;
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0.f;
                     }
-                    if (two) {
-                        float o1[32];
-                        tmem_ld32(t_lane + C::O_COL + 128 + c, o1);
-                        tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = fmaf(o1[e], w1, o[e]);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) odd = fmaf(o[e], 0.f, odd);
+                    for (int e = 0; e < 32; e += 2)
+                        odd = fma2(make_float2(o[e], o[e + 1]), make_float2(0.f, 0.f), odd);
                     if (row < rows) {
                         if (whole) {
 #pragma unroll
@@ -1018,7 +1042,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     tc_fence_before();
                     arrive(C::X_EMPTY);
                 }
-                uint32_t again = __ballot_sync(0xffffffffu, row < rows && nt > 0 && !(odd == 0.f && l == l));
+                uint32_t again = __ballot_sync(0xffffffffu, row < rows && nt > 0 && !(odd.x + odd.y == 0.f && l == l));
                 __syncwarp();
                 while (again) {
                     const int r = __ffs(again) - 1;
