@@ -436,10 +436,10 @@ int decode_impl(void* out, const void* q, const void* k_cache, const void* v_cac
 
 namespace {
 
-// Workspace of the multi-query attention: one counter per CTA of the grid
+// Workspace of the multi-query attention: eight counters per CTA of the grid
 // (zero between launches), in a region of its own whatever kernel the call
 // runs on, then the partial results, two per CTA.
-constexpr int kAttnCounters = 512;
+constexpr int kAttnCounters = 8 * 2 * pkv::kAttnSms;
 struct AttnLayout {
     pkv::AttnShape shape;
     int part_rows;
@@ -451,7 +451,7 @@ AttnLayout attn_layout(long long num_tokens, long long group, long long D, int k
     w.shape = kv_dtype == PKV_F32 ? pkv::attn_simt_shape() : pkv::attn_tc_shape();
     w.part_rows = num_tokens * group < w.shape.rows ? (int)(num_tokens * group) : w.shape.rows;
     const size_t rows = size_t(2) * w.shape.grid * w.part_rows;
-    w.ml_off = kAttnCounters * sizeof(int);
+    w.ml_off = align256(kAttnCounters * sizeof(int));
     w.o_off = w.ml_off + align256(rows * sizeof(float2));
     w.total = w.o_off + align256(rows * D * sizeof(float));
     return w;

@@ -38,7 +38,8 @@ struct AttnParams {
     const int32_t* parents;  // tree attention: parent of each draft in its sequence, or -1; else null
     const float* k_scales;   // fp8 caches, else null
     const float* v_scales;
-    int* counters;           // [gridDim.x] parts finished of the item whose first part the CTA owns; zero between launches
+    int* counters;           // [gridDim.x][8] parts finished of the item whose first part the CTA owns (of all
+                             // its rows, or of each warp's); zero between launches
     float2* ws_ml;           // [2 gridDim.x][part_rows] (maximum in log2 units, sum)
     float4* ws_o;            // [2 gridDim.x][D / 4][part_rows]: neighbouring rows side by side
     int* err;
@@ -321,7 +322,7 @@ __device__ __forceinline__ bool attn_merge(const AttnParams& p, const AttnItem& 
     __threadfence();
     if (!sync()) return false;
     if (tid == 0) {
-        int* count = p.counters + Walk::owner(it.at, it.keys, share, 0);
+        int* count = p.counters + Walk::owner(it.at, it.keys, share, 0) * 8;
         const int last = atomicAdd(count, 1) == it.nparts - 1;
         if (last) *count = 0;
         *flag = last;

@@ -11,7 +11,7 @@ namespace pkv {
 
 constexpr int kAttnSms = 148;
 
-// The workspace holds 512 counters: no grid is larger.
+// No grid is larger than two CTAs per SM: the workspace has counters for those.
 
 // What a launch asks of its workspace: CTAs of the grid (two partial results
 // each) and rows of a full tile.

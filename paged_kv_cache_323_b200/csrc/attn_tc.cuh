@@ -251,6 +251,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+// 32 bytes of a lane's own, both halves of one sector at once.
+__device__ __forceinline__ void store_sector(void* to, const uint32_t (&r)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -261,13 +268,13 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 // total.  One pair in POLY_OF goes by ex2_poly, so that the special-function
 // unit (a quarter of the lanes a clock) and the FMA pipe share the work.
 constexpr int POLY_OF = 8;
-template <bool FP8, int N>
+template <bool FP8, int N, bool POLY = true>
 __device__ __forceinline__ void weights(const float* x, float2 q, float2 m, uint32_t* pk, float2& sum) {
     float2 sum1 = make_float2(0.f, 0.f);
 #pragma unroll
     for (int c = 0; c < N / 2; ++c) {
         float2 y = fma2(make_float2(x[2 * c], x[2 * c + 1]), q, m);
-        if (c % POLY_OF == POLY_OF - 1) {
+        if (POLY && c % POLY_OF == POLY_OF - 1) {
             y = ex2_poly(y);
         } else {
             y.x = ex2(y.x);
@@ -310,7 +317,7 @@ struct Cfg {
     static constexpr int NRAW = FP8 ? (D == 128 ? 4 : 8) : 0;
     static constexpr int NLOAD = FP8 ? NRAW : NSLOT;  // slots that TMA fills
     static constexpr int THREADS = FP8 ? 512 : 384;
-    static constexpr int ITEMS = 4;                 // items the walk is ahead
+    static constexpr int ITEMS = FP8 ? 2 : 4;       // items the walk is ahead
     // registers: what the launch gives all threads, and its split among roles
     static constexpr int REGS_SOFTMAX = FP8 ? 176 : 216;
     static constexpr int REGS_ISSUE = FP8 ? 64 : 72;
@@ -344,7 +351,7 @@ struct Cfg {
     static constexpr int SYNC_BAR = ITEM_EMPTY + 8 * ITEMS, MMA_DONE = SYNC_BAR + 8;
     static_assert(MMA_DONE + 8 == BAR_OFF + NBARS * 8, "");
     static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;  // tmem address, abort, flag, turns
-    static constexpr int ITEM_OFF = (MISC_OFF + 16 + 15) / 16 * 16;
+    static constexpr int ITEM_OFF = (MISC_OFF + 48 + 15) / 16 * 16;
     static constexpr int WALK_OFF = ITEM_OFF + ITEMS * 64;
     static constexpr int ML_OFF = WALK_OFF + (THREADS / 32 + 8) * 8;  // float2[128]
     static constexpr int QS_OFF = ML_OFF + 128 * 8;                    // 256 exponents, fp8
@@ -352,6 +359,10 @@ struct Cfg {
     static_assert(SMEM_BYTES <= 232448, "227 KB of shared memory");
     static_assert(sizeof(AttnItem) <= 64, "");
 };
+
+// An item of at most this many parts is joined by the warps that have its
+// rows; more go over all threads (attn_merge).
+constexpr int FEW_PARTS = 4;
 
 // What an item asks of the two pipelines.
 struct Plan {
@@ -491,7 +502,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
     int* merge_flag = reinterpret_cast<int*>(smem + C::MISC_OFF + 8);
-    int* turns = reinterpret_cast<int*>(smem + C::MISC_OFF + 12);  // split items this CTA has counted
+    int* turns = reinterpret_cast<int*>(smem + C::MISC_OFF + 16);  // [8] split items each softmax warp has counted
     float2* ml_x = reinterpret_cast<float2*>(smem + C::ML_OFF);
     unsigned char* q_row_scale = smem + C::QS_OFF;  // biased exponents
 
@@ -526,7 +537,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
         init(C::SYNC_BAR, 8);
         init(C::MMA_DONE, 1);
         *abort_flag = 0;
-        *turns = 0;
+        for (int i = 0; i < 8; ++i) turns[i] = 0;
         fence_mbarrier_init();
     }
     if (warp == 9) {
@@ -648,8 +659,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             }
         } else if (warp == 9) {
             // ------------------------------------------------------ MMA issue
-            // Every instruction here counts: between two products the tensor cores
-            // wait for this warp, whose instructions are fetched anew each time.
+            // The tensor cores hold a few instructions in advance, some 250 clocks of work.
+            // What this warp does between two of them has to fit into that, so waits and
+            // bookkeeping are spread: after six of a product's eight, between two products
+            // and in the middle of QK^T.
             const uint32_t one = elect_one();
             // descriptors of the first tile; others differ in the address field (16-byte units)
             const uint64_t q_desc = sw128_desc(sb + C::Q_OFF, 16, 1024),
@@ -668,28 +681,29 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 if (++slot == C::NSLOT) slot = 0, slot_phase ^= 1;
                 return st;
             };
-            auto qk = [&](int i, uint32_t q_tile, uint32_t st) {
+            auto release = [&](uint32_t st) { commit_one(sb + C::SLOT_EMPTY + 8 * st, one); };
+            // half 0 and half 1 of S_i = Q K^T
+            auto qk = [&](int i, uint32_t q_tile, uint32_t st, int half) {
                 const uint32_t a = q_lo + q_tile * (C::QTILE >> 4), b = k_lo + st * (C::TILE >> 4);
+                constexpr int N = D / 32;
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
+                for (int k = 0; k < N; ++k) {
+                    const int kk = half * N + k;
                     mma_ss(tmem + i * 128, a + (((kk >> 2) * C::QHALF + (kk & 3) * 32) >> 4), q_hi,
                            b + (((kk >> 2) * C::HSTEP + (kk & 3) * 32) >> 4), k_hi, idesc_qk, kk > 0, one);
-                commit_one(sb + C::S_FULL + 8 * i, one);
+                }
+                if (half == 1) commit_one(sb + C::S_FULL + 8 * i, one);
             };
-            auto pv = [&](int i, uint32_t st, uint32_t phase, uint32_t accumulate) {
+            // keys 0 .. 95 and 96 .. 127 of O_i += P V
+            auto pv = [&](int i, uint32_t st, uint32_t phase, uint32_t accumulate, int part) {
                 const uint32_t b = v_lo + st * (C::TILE >> 4);
-                ok = ok && wait(C::P_FULL + 8 * i, phase);
+                ok = ok && wait((part == 0 ? C::P_FULL : C::P_REST) + 8 * i, phase);
                 if (!ok) return;
                 tc_fence_after();
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {
-                    if (kk == 6) {
-                        if (!(ok = wait(C::P_REST + 8 * i, phase))) return;
-                        tc_fence_after();
-                    }
+                for (int kk = part == 0 ? 0 : 6; kk < (part == 0 ? 6 : 8); ++kk)
                     mma_ts(tmem + C::O_COL + i * 128, tmem + i * 128 + kk * 8, b + ((kk * 2 * C::GSTRIDE) >> 4), v_hi,
                            C::IDESC_PV, kk > 0 ? 1u : accumulate, one);
-                }
             };
             AttnItem u;
             for (int n = 0; ok && take_item(n, u); ++n) {
@@ -705,51 +719,62 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 uint32_t ks = next_load(), vs = 0;
                 if (!ok) break;
                 tc_fence_after();
-                if (n0 > 0) qk(0, 0, ks);
+                if (n0 > 0) {
+                    qk(0, 0, ks, 0);
+                    qk(0, 0, ks, 1);
+                }
                 if (!wide) {
-                    commit_one(sb + C::SLOT_EMPTY + 8 * ks, one);
+                    release(ks);
                     --left;
                     if (n1 > 0) ks = next_load();
                     if (!ok) break;
                 }
                 if (n1 > 0) {
-                    qk(1, wide, ks);
-                    commit_one(sb + C::SLOT_EMPTY + 8 * ks, one);
+                    qk(1, wide, ks, 0);
+                    qk(1, wide, ks, 1);
+                    release(ks);
                     --left;
                 }
                 if (left == 0) commit_one(sb + C::Q_EMPTY, one);
+                vs = next_load();
                 const int nmax = n0 > n1 ? n0 : n1;
                 for (int t = 0; t < nmax; ++t) {
                     if (t < n0) {
-                        vs = next_load();
-                        if (t + 1 < n0) ks = next_load();
-                        pv(0, vs, p_phase0, t > 0);
+                        const bool more = t + 1 < n0;
+                        pv(0, vs, p_phase0, t > 0, 0);
+                        if (more) ks = next_load();
+                        pv(0, vs, p_phase0, t > 0, 1);
                         if (!ok) break;
                         p_phase0 ^= 1;
-                        if (!wide) commit_one(sb + C::SLOT_EMPTY + 8 * vs, one);
-                        if (t + 1 < n0) {
-                            qk(0, 0, ks);
+                        if (more) qk(0, 0, ks, 0);
+                        else commit_one(sb + C::O_FULL, one);
+                        if (!wide) {
+                            release(vs);
+                            if (t < n1) vs = next_load();
+                        }
+                        if (more) {
+                            qk(0, 0, ks, 1);
                             if (!wide) {
-                                commit_one(sb + C::SLOT_EMPTY + 8 * ks, one);
+                                release(ks);
                                 if (--left == 0) commit_one(sb + C::Q_EMPTY, one);
                             }
-                        } else {
-                            commit_one(sb + C::O_FULL, one);
                         }
                     }
                     if (t < n1) {
-                        if (!wide || t >= n0) vs = next_load();
-                        if (t + 1 < n1 && (!wide || t + 1 >= n0)) ks = next_load();
-                        pv(1, vs, p_phase1, t > 0);
+                        const bool more = t + 1 < n1;
+                        pv(1, vs, p_phase1, t > 0, 0);
+                        if (more && (!wide || t + 1 >= n0)) ks = next_load();
+                        pv(1, vs, p_phase1, t > 0, 1);
                         if (!ok) break;
                         p_phase1 ^= 1;
-                        commit_one(sb + C::SLOT_EMPTY + 8 * vs, one);
-                        if (t + 1 < n1) {
-                            qk(1, wide, ks);
-                            commit_one(sb + C::SLOT_EMPTY + 8 * ks, one);
+                        if (more) qk(1, wide, ks, 0);
+                        else commit_one(sb + C::O_FULL + 8, one);
+                        release(vs);
+                        if (more || t + 1 < n0) vs = next_load();
+                        if (more) {
+                            qk(1, wide, ks, 1);
+                            release(ks);
                             if (--left == 0) commit_one(sb + C::Q_EMPTY, one);
-                        } else {
-                            commit_one(sb + C::O_FULL + 8, one);
                         }
                     }
                 }
@@ -825,7 +850,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 s_phase ^= 1;
                 tc_fence_after();
                 const bool short_step = k0 + C::KEYS > u.kv1 || bad != 0;
-                const bool masked = short_step || k0 + C::KEYS > clear;
+                bool masked = short_step || k0 + C::KEYS > clear;
                 uint32_t w[4];
                 if (masked) {
                     uint32_t there[4];
@@ -833,6 +858,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     there_words(u.kv1 - k0, bad, bs, there);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) w[c] &= there[c];
+                    masked = __any_sync(0xffffffffu, (w[0] & w[1] & w[2] & w[3]) != 0xffffffffu);
                     if (!FP8 && short_step && (!plan.wide || wg == 0 || j >= plan.n0)) {
                         // keys that are not there: their rows of V may hold anything
                         const int li = base + plan.v_load(j), st = li % C::NSLOT;
@@ -891,26 +917,29 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     stale = false;
                 }
                 float2 sum = make_float2(0.f, 0.f);
-                if (masked || t == 0 || __any_sync(0xffffffffu, m == -INFINITY)) {
-                    // steps with masks or without a reference, in a short loop
+                if (masked || (t > 0 && __any_sync(0xffffffffu, m == -INFINITY))) {
+                    // steps with masks, in a short loop; of its 32 keys a warp's rows mostly see
+                    // all or none
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
-                        float x[32];
                         uint32_t pk[16];
-                        tmem_ld32(t_s + 32 * c, x);
-                        tmem_wait_ld();
                         const uint32_t word = !masked ? 0xffffffffu : c == 0 ? w[0] : c == 1 ? w[1] : c == 2 ? w[2] : w[3];
-                        mask32(x, word);
-                        // the first keys that a row sees give its reference
-                        if (!FP8 && __any_sync(0xffffffffu, m == -INFINITY)) {
-                            const float mx = largest32(x, -INFINITY) * qa;
-                            m = m == -INFINITY ? mx : m;
-                        }
-                        const float mm = m == -INFINITY ? 0.f : -m;
-                        weights<FP8, 32>(x, q2, make_float2(mm, mm), pk, sum);
+                        if (__any_sync(0xffffffffu, word != 0u)) {
+                            float x[32];
+                            tmem_ld32(t_s + 32 * c, x);
+                            tmem_wait_ld();
+                            if (!__all_sync(0xffffffffu, word == 0xffffffffu)) mask32(x, word);
+                            // the first keys that a row sees give its reference
+                            if (!FP8 && __any_sync(0xffffffffu, m == -INFINITY)) {
+                                const float mx = largest32(x, -INFINITY) * qa;
+                                m = m == -INFINITY ? mx : m;
+                            }
+                            const float mm = m == -INFINITY ? 0.f : -m;
+                            weights<FP8, 32, false>(x, q2, make_float2(mm, mm), pk, sum);  // exactly 0 where masked
+                        } else {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)  // no weight at all, not 2^-125
-                            pk[e] &= (word & (1u << 2 * e) ? 0xffffu : 0u) | (word & (2u << 2 * e) ? 0xffff0000u : 0u);
+                            for (int e = 0; e < 16; ++e) pk[e] = 0u;
+                        }
                         tmem_st16(t_s + 16 * c, pk);  // over scores that have been read
                         if (c == 2) {
                             tmem_wait_st();
@@ -925,13 +954,17 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, x + 32 * c);
                     tmem_wait_ld();
+                    if (t == 0) {
+                        if (!FP8) m = largest32(x, -INFINITY) * qa;  // the row's reference
+                        if (!(ok = o_readable())) break;
+                    }
                     const float2 m2 = make_float2(-m, -m);
-                    weights<FP8, 96>(x, q2, m2, pk, sum);
+#pragma unroll
+                    for (int c = 0; c < 3; ++c) weights<FP8, 32>(x + 32 * c, q2, m2, pk + 16 * c, sum);
                     tmem_st32(t_s, pk);
                     tmem_st16(t_s + 32, pk + 32);
                     tmem_wait_st();
-                    // the product of the first 96 keys may start (a step that is not the
-                    // item's first: o_readable has been asked)
+                    // the product of the first 96 keys may start
                     tc_fence_before();
                     arrive(C::P_FULL + 8 * wg);
                     weights<FP8, 32>(x + 96, q2, m2, pk, sum);
@@ -991,79 +1024,198 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     if (plan.n1 > 0) o_phase[1] ^= 1;
                 }
                 tc_fence_after();
-                const bool whole = u.nparts == 1;
-                const float inv = whole ? (l == 0.f ? 0.f : vs / l) : vs;  // no key seen: a zero row
-                w0 *= inv;
-                w1 *= inv;
-                __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
-                                     ((long long)(u.row + (row >> gl)) * p.num_heads + u.g * G + (row & (G - 1))) * D;
+                const int rows_left = rows - row0;  // of this warp
+                const bool here = row < rows;
+                const bool split = u.nparts > 1, few = u.nparts <= FEW_PARTS;
                 const int slot = attn_partial(blockIdx.x, u.part);
-                float2 odd = make_float2(0.f, 0.f);  // becomes NaN with the first value that is not finite
-#pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    float o[32];
-                    if (nt > 0) {
-                        tmem_ld32(t_o + c, o);
-                        if (two) {
-                            float o1[32];
-                            tmem_ld32(t_lane + C::O_COL + 128 + c, o1);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = fmaf(o1[e], w1, o[e] * w0);
-                        } else {
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] *= w0;
-                        }
-                    } else {
+                int* count = split ? p.counters + AttnWalk<TcDivision>::owner(u.at, u.keys, walk0.share, 0) * 8 + (warp & 7)
+                                   : nullptr;
+                // A whole item: o / l.  Part of a split one: o, with its m and l.
+                w0 *= split ? vs : l == 0.f ? 0.f : vs / l;  // no key seen: a zero row
+                w1 *= split ? vs : l == 0.f ? 0.f : vs / l;
+                auto own = [&](int c, float* o) {  // 32 dims of this part
+                    if (nt == 0) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                        return;
                     }
+                    tmem_ld32(t_o + c, o);
+                    if (two) {
+                        float o1[32];
+                        tmem_ld32(t_lane + C::O_COL + 128 + c, o1);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = fmaf(o1[e], w1, o[e] * w0);
+                    } else {
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] *= w0;
+                    }
+                };
+                __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
+                                     ((long long)(u.row + (row >> gl)) * p.num_heads + u.g * G + (row & (G - 1))) * D;
+                const bool sectors = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
+                auto store32 = [&](__nv_bfloat16* to, const float* o) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 16) {
+                        uint32_t r[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) r[i] = pack_bf16(o[e + 2 * i], o[e + 2 * i + 1]);
+                        if (sectors) {
+                            store_sector(to + e, r);
+                        } else {
+                            *reinterpret_cast<uint4*>(to + e) = make_uint4(r[0], r[1], r[2], r[3]);
+                            *reinterpret_cast<uint4*>(to + e + 8) = make_uint4(r[4], r[5], r[6], r[7]);
+                        }
+                    }
+                };
+                float2 odd = make_float2(0.f, 0.f);  // becomes NaN with the first value that is not finite
+                auto look = [&](const float* o) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 2)
                         odd = fma2(make_float2(o[e], o[e + 1]), make_float2(0.f, 0.f), odd);
-                    if (row < rows) {
-                        if (whole) {
+                };
+                auto odd_rows = [&]() {
+                    return __ballot_sync(0xffffffffu, here && nt > 0 && !(odd.x + odd.y == 0.f && l == l));
+                };
+                if (!split) {
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        float o[32];
+                        own(c, o);
+                        look(o);
+                        if (here) store32(dst + c, o);
+                    }
+                    uint32_t again = odd_rows();
+                    __syncwarp();
+                    while (again) {
+                        const int r = row0 + __ffs(again) - 1;
+                        again &= again - 1;
+                        float ms, ls, acc[D / 32];
+                        slow_row<D, FP8>(p, u, r, ms, ls, acc);
+                        __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) +
+                                            ((long long)(u.row + (r >> gl)) * p.num_heads + u.g * G + (r & (G - 1))) * D;
 #pragma unroll
-                            for (int e = 0; e < 32; e += 8)
-                                *reinterpret_cast<uint4*>(dst + c + e) =
-                                    make_uint4(pack_bf16(o[e], o[e + 1]), pack_bf16(o[e + 2], o[e + 3]),
-                                               pack_bf16(o[e + 4], o[e + 5]), pack_bf16(o[e + 6], o[e + 7]));
-                        } else {
+                        for (int e = 0; e < D / 32; ++e)
+                            to[lane * (D / 32) + e] = __float2bfloat16_rn(ls == 0.f ? 0.f : acc[e] / ls);
+                    }
+                } else if (rows_left > 0) {
+                    // With few parts each warp joins its own rows: the last of an item's parts to
+                    // come has the others' results at hand and needs not write its own.
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        float o[32];
+                        own(c, o);
+                        look(o);
+                    }
+                    uint32_t again = odd_rows();
+                    int seen = 0;
+                    if (few && lane == 0) asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(seen) : "l"(count) : "memory");
+                    seen = __shfl_sync(0xffffffffu, seen, 0);
+                    bool last = few && seen == u.nparts - 1;
+                    const bool written = !last || again != 0;
+                    if (written) {
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            float o[32];
+                            own(c, o);
+                            if (here) {
 #pragma unroll
-                            for (int e = 0; e < 32; e += 4)
-                                p.ws_o[attn_partial_at(p, slot, D, c + e, row)] =
-                                    make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                                for (int e = 0; e < 32; e += 4)
+                                    p.ws_o[attn_partial_at(p, slot, D, c + e, row)] =
+                                        make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                            }
+                        }
+                        if (here) p.ws_ml[(long long)slot * p.part_rows + row] = make_float2(m, l);
+                        __syncwarp();
+                        while (again) {
+                            const int r = row0 + __ffs(again) - 1;
+                            again &= again - 1;
+                            float ms, ls, acc[D / 32];
+                            slow_row<D, FP8>(p, u, r, ms, ls, acc);
+#pragma unroll
+                            for (int e = 0; e < D / 32; ++e)
+                                reinterpret_cast<float*>(p.ws_o + attn_partial_at(p, slot, D, lane * (D / 32), r))
+                                    [(lane * (D / 32)) % 4 + e] = acc[e];
+                            if (lane == 0) p.ws_ml[(long long)slot * p.part_rows + r] = make_float2(ms, ls);
+                        }
+                    }
+                    if (few) {
+                        if (!last) {
+                            __threadfence();
+                            __syncwarp();
+                            if (lane == 0) seen = atomicAdd(count, 1);
+                            last = __shfl_sync(0xffffffffu, seen, 0) == u.nparts - 1;
+                        }
+                        if (lane == 0) {
+                            if (last) *count = 0;
+                            turns[warp] += 1;
+                        }
+                        if (last) {
+                            __threadfence();
+                            // M = max m_i, out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i, in the parts' order
+                            float wi[FEW_PARTS], M = -INFINITY, L = 0.f;
+                            const float4* from[FEW_PARTS];
+                            float li[FEW_PARTS];
+#pragma unroll
+                            for (int i = 0; i < FEW_PARTS; ++i) {
+                                wi[i] = -INFINITY;
+                                li[i] = 0.f;
+                                from[i] = nullptr;
+                                if (i >= u.nparts || !here) continue;
+                                float2 ml = make_float2(m, l);
+                                if (i != u.part || written) {
+                                    const int si = attn_partial(AttnWalk<TcDivision>::owner(u.at, u.keys, walk0.share, i), i);
+                                    ml = __ldcg(&p.ws_ml[(long long)si * p.part_rows + row]);
+                                    from[i] = p.ws_o + attn_partial_at(p, si, D, 0, row);
+                                }
+                                wi[i] = ml.x;
+                                li[i] = ml.y;
+                                M = fmaxf(M, ml.x);
+                            }
+#pragma unroll
+                            for (int i = 0; i < FEW_PARTS; ++i) {
+                                // no key seen in any part: all sums are 0 (or NaN), taken as they are
+                                wi[i] = M == -INFINITY ? 1.f : ex2(wi[i] - M);
+                                L = fmaf(wi[i], li[i], L);
+                            }
+                            const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 32) {
+                                float o[32], x[32];
+                                own(c, x);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] = 0.f;
+#pragma unroll
+                                for (int i = 0; i < FEW_PARTS; ++i) {
+                                    if (i >= u.nparts) continue;
+                                    float4 v[8];
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e)
+                                        v[e] = from[i] != nullptr
+                                                   ? __ldcg(from[i] + (c / 4 + e) * (long long)p.part_rows)
+                                                   : make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e) {
+                                        o[4 * e] = fmaf(wi[i], v[e].x, o[4 * e]);
+                                        o[4 * e + 1] = fmaf(wi[i], v[e].y, o[4 * e + 1]);
+                                        o[4 * e + 2] = fmaf(wi[i], v[e].z, o[4 * e + 2]);
+                                        o[4 * e + 3] = fmaf(wi[i], v[e].w, o[4 * e + 3]);
+                                    }
+                                }
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] *= inv;
+                                if (here) store32(dst + c, o);
+                            }
                         }
                     }
                 }
-                if (!whole && row < rows) p.ws_ml[(long long)slot * p.part_rows + row] = make_float2(m, l);
                 if (two) {  // the other pipeline's O may be written again
                     tc_fence_before();
                     arrive(C::X_EMPTY);
                 }
-                uint32_t again = __ballot_sync(0xffffffffu, row < rows && nt > 0 && !(odd.x + odd.y == 0.f && l == l));
-                __syncwarp();
-                while (again) {
-                    const int r = __ffs(again) - 1;
-                    again &= again - 1;
-                    float ms, ls, acc[D / 32];
-                    slow_row<D, FP8>(p, u, row0 + r, ms, ls, acc);
-                    const int rr = row0 + r;
-                    __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) +
-                                        ((long long)(u.row + (rr >> gl)) * p.num_heads + u.g * G + (rr & (G - 1))) * D;
-#pragma unroll
-                    for (int e = 0; e < D / 32; ++e) {
-                        if (whole)
-                            to[lane * (D / 32) + e] = __float2bfloat16_rn(ls == 0.f ? 0.f : acc[e] / ls);
-                        else
-                            reinterpret_cast<float*>(p.ws_o + attn_partial_at(p, slot, D, lane * (D / 32), rr))
-                                [(lane * (D / 32)) % 4 + e] = acc[e];
-                    }
-                    if (!whole && lane == 0) p.ws_ml[(long long)slot * p.part_rows + rr] = make_float2(ms, ls);
-                }
             }
-            if (u.nparts > 1) {
+            if (u.nparts > FEW_PARTS) {
                 if (!(ok = attn_merge<TcDivision, __nv_bfloat16, D, 256>(p, u, walk0.share, merge_flag, turns, tid, sync)))
                     break;
             }
@@ -1199,15 +1351,19 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
         // parts that were not counted: empty ones, so that the counters end at zero
         AttnWalk<TcDivision> walk =
             attn_walk_start<TcDivision, C::THREADS>(p, reinterpret_cast<long long*>(smem + C::WALK_OFF));
-        if (tid == 0) {
+        if (warp < 8 && lane == 0) {
             AttnItem u;
             int k = 0;
             while (walk.next(p, u)) {
-                if (u.nparts == 1 || k++ < *turns) continue;
-                for (int r = 0; r < (u.ntok << gl); ++r)
+                const int n_rows = u.ntok << gl, first_row = n_rows > 128 ? warp * 32 : (warp & 3) * 32;
+                const bool few = u.nparts <= FEW_PARTS;
+                if (u.nparts == 1 || (few ? first_row >= n_rows || (n_rows <= 128 && warp >= 4) : warp > 0)) continue;
+                if (k++ < turns[warp]) continue;
+                const int n = few && n_rows > first_row + 32 ? first_row + 32 : n_rows;
+                for (int r = few ? first_row : 0; r < n; ++r)
                     p.ws_ml[(long long)attn_partial(blockIdx.x, u.part) * p.part_rows + r] = make_float2(-INFINITY, 0.f);
                 __threadfence();
-                int* c = p.counters + AttnWalk<TcDivision>::owner(u.at, u.keys, walk.share, 0);
+                int* c = p.counters + AttnWalk<TcDivision>::owner(u.at, u.keys, walk.share, 0) * 8 + warp;
                 if (atomicAdd(c, 1) == u.nparts - 1) *c = 0;
             }
         }
