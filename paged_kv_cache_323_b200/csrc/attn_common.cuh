@@ -58,14 +58,18 @@ struct AttnParams {
 };
 
 // ------------------------------------------------------------ the division
-// ROWS: rows of a tile.  A call whose share per CTA is at least COARSE keys
-// cuts items at multiples of FINE keys (balance); a smaller call cuts them at
-// multiples of COARSE only (a part shorter than that costs more in its merge
-// than it saves).  ITEM: cost of an item besides its keys, in keys.
-template <int ROWS_, int FINE_, int COARSE_, int ITEM_>
+// ROWS: rows of a tile.  Work is counted in the time that one key takes a tile
+// of at most HALF rows; a larger tile takes TWICE of it.  An item whose share
+// of a CTA is at least COARSE keys is cut at multiples of FINE keys (balance),
+// in smaller calls items are cut at multiples of COARSE only (a part shorter
+// than that costs more in its merge than it saves).  ITEM: work of an item
+// besides its keys.
+template <int ROWS_, int HALF_, int TWICE_, int FINE_, int COARSE_, int ITEM_>
 struct AttnDivision {
-    static constexpr int ROWS = ROWS_, FINE = FINE_, COARSE = COARSE_, ITEM = ITEM_;
+    static constexpr int ROWS = ROWS_, HALF = HALF_, TWICE = TWICE_, FINE = FINE_, COARSE = COARSE_, ITEM = ITEM_;
     static_assert(COARSE % FINE == 0 && (FINE & (FINE - 1)) == 0 && (COARSE & (COARSE - 1)) == 0, "");
+    static constexpr int FULL = ROWS > HALF ? TWICE : 1;  // work per key of a full tile
+    __host__ __device__ static constexpr int per_key(int rows) { return rows > HALF ? TWICE : 1; }
 };
 
 // Sequence s of a launch: its rows, and what its tiles cost.
@@ -89,11 +93,20 @@ struct AttnSeq {
         const long long end = (long long)(t + 1) * tt;
         return first + (end < n ? (int)end : n);
     }
-    // cost of the tiles before tile t, for one kv head
-    __device__ __forceinline__ long long before(int t, int tt, int item) const {
-        if (!valid) return (long long)t * item;
-        long long c = (long long)t * (first + item) + (long long)tt * t * (t + 1) / 2;
-        if ((long long)t * tt > n) c -= (long long)t * tt - n;  // t past the last tile
+    // work per key of tile t
+    template <class Div>
+    __device__ __forceinline__ int per_key(int t, int tt, int group_log2) const {
+        return Div::per_key((n - t * tt < tt ? n - t * tt : tt) << group_log2);
+    }
+    // work of the tiles before tile t, for one kv head
+    template <class Div>
+    __device__ __forceinline__ long long before(int t, int tt, int group_log2) const {
+        const int last = tiles(tt) - 1;
+        const int full = t <= last ? t : last;  // tiles that are surely full
+        if (full < 0) return 0;
+        long long c = (long long)full * Div::ITEM;
+        if (valid) c += Div::FULL * ((long long)full * first + (long long)tt * full * (full + 1) / 2);
+        if (t > last) c += (long long)keys(last, tt) * per_key<Div>(last, tt, group_log2) + Div::ITEM;
         return c;
     }
 };
@@ -108,6 +121,7 @@ struct AttnItem {
     int g;         // kv head
     int part, nparts;
     int keys;      // keys of the whole item
+    int per_key;   // work of each
     long long at;  // start of the item in the launch's work
 };
 
@@ -117,33 +131,32 @@ struct AttnWalk {
     int tt, s, t, g;
     AttnSeq q;
 
-    // offset (in keys) at which a boundary `o` past the item's start cuts an item of K keys
-    __device__ __forceinline__ static int cut(long long o, int K, long long share) {
+    // key at which a boundary `o` past the start of an item of K keys, f each, cuts it
+    __device__ __forceinline__ static int cut(long long o, int K, int f, long long share) {
         if (o <= 0) return 0;
-        if (o >= K) return K;
-        if (share >= Div::COARSE) return (int)o & ~(Div::FINE - 1);
+        if (o >= (long long)K * f) return K;
+        const int k = (int)o / f;
+        if (share >= Div::COARSE * f) return k & ~(Div::FINE - 1);
         const int most = K > Div::COARSE ? K - Div::COARSE : 0;  // no part shorter than COARSE
-        return (o < most ? (int)o : most) & ~(Div::COARSE - 1);
+        return (k < most ? k : most) & ~(Div::COARSE - 1);
     }
-    // CTA that owns part i of the item (at, K).  With a share of at least
-    // COARSE, a multiple of FINE, the cuts after the first are `share` apart;
-    // with a smaller one every multiple of COARSE up to K - COARSE is cut, and
-    // a part belongs to the last CTA that starts before the part's end.
-    __device__ __forceinline__ static int owner(long long at, int K, long long share, int i) {
-        if (share >= Div::COARSE) {
-            const int b0 = (int)(at / share);
-            const long long o1 = (b0 + 1) * share - at;
-            return b0 + i + (o1 < Div::FINE && o1 < K ? 1 : 0);
-        }
-        const int e = i + 1 < parts(at, K, share) ? (i + 1) * Div::COARSE : K;
-        const long long b0 = at / share;
-        return (int)b0 + (int)(((unsigned)(at - b0 * share) + (unsigned)e - 1u) / (unsigned)share);
+    // CTA that owns part i of the item (at, K, f).  With a share of at least
+    // COARSE keys every boundary but one short of FINE keys makes a cut; with a
+    // smaller one every multiple of COARSE up to K - COARSE is cut, and a part
+    // belongs to the last CTA that starts before the part's end.
+    __device__ __forceinline__ static int owner(const AttnItem& it, long long share, int i) {
+        const int b0 = (int)(it.at / share), f = it.per_key, K = it.keys;
+        const long long o1 = (b0 + 1) * share - it.at;
+        if (share >= Div::COARSE * f) return b0 + i + (o1 < Div::FINE * f && o1 < (long long)K * f ? 1 : 0);
+        const long long e = i + 1 < parts(it, share) ? (long long)(i + 1) * Div::COARSE * f : (long long)K * f;
+        return b0 + (int)((it.at - b0 * share + e - 1) / share);
     }
-    __device__ __forceinline__ static int parts(long long at, int K, long long share) {
-        if (share >= Div::COARSE) {
-            const long long o1 = (at / share + 1) * share - at;
-            if (o1 >= K) return 1;
-            return (o1 >= Div::FINE ? 2 : 1) + (int)((K - 1 - o1) / share);
+    __device__ __forceinline__ static int parts(const AttnItem& it, long long share) {
+        const int f = it.per_key, K = it.keys;
+        if (share >= Div::COARSE * f) {
+            const long long o1 = (it.at / share + 1) * share - it.at, all = (long long)K * f;
+            if (o1 >= all) return 1;
+            return (o1 >= Div::FINE * f ? 2 : 1) + (int)((all - 1 - o1) / share);
         }
         return K < Div::COARSE ? 1 : K / Div::COARSE;
     }
@@ -151,10 +164,10 @@ struct AttnWalk {
     // The next item with work for this CTA.
     __device__ bool next(const AttnParams& p, AttnItem& it) {
         while (at < end) {
-            const int K = q.keys(t, tt);
-            const long long c = K + Div::ITEM, a = begin - at;
-            const int k0 = cut(a, K, share);
-            const int k1 = at + c <= end ? K : cut(end - at, K, share);
+            const int K = q.keys(t, tt), f = q.template per_key<Div>(t, tt, p.group_log2);
+            const long long c = (long long)K * f + Div::ITEM, a = begin - at;
+            const int k0 = cut(a, K, f, share);
+            const int k1 = at + c <= end ? K : cut(end - at, K, f, share);
             const bool mine = K == 0 ? a <= 0 : k0 < k1;
             if (mine) {
                 it.seq = s;
@@ -166,14 +179,14 @@ struct AttnWalk {
                 it.kv1 = k1;
                 it.g = g;
                 it.keys = K;
+                it.per_key = f;
                 it.at = at;
                 it.nparts = 1;
                 it.part = 0;
                 if (k0 > 0 || k1 < K) {
-                    it.nparts = parts(at, K, share);
-                    const int b0 = owner(at, K, share, 0);
-                    // in the first regime the parts' owners follow one another
-                    it.part = share >= Div::COARSE ? (int)blockIdx.x - b0 : k0 / Div::COARSE;
+                    it.nparts = parts(it, share);
+                    // with large shares the parts' owners follow one another
+                    it.part = share >= Div::COARSE * f ? (int)blockIdx.x - owner(it, share, 0) : k0 / Div::COARSE;
                 }
             }
             at += c;
@@ -210,7 +223,7 @@ __device__ __forceinline__ AttnWalk<Div> attn_walk_start(const AttnParams& p, lo
     for (int s = s0; s < s1; ++s) {
         AttnSeq q;
         q.load(p, s, blockIdx.x == 0);
-        mine += q.before(q.tiles(w.tt), w.tt, Div::ITEM) * p.num_kv_heads;
+        mine += q.before<Div>(q.tiles(w.tt), w.tt, p.group_log2) * p.num_kv_heads;
     }
     long long incl = mine;
 #pragma unroll
@@ -228,7 +241,6 @@ __device__ __forceinline__ AttnWalk<Div> attn_walk_start(const AttnParams& p, lo
         total += scratch[i];
     }
     long long share = (total + gridDim.x - 1) / gridDim.x;
-    if (share >= Div::COARSE) share = (share + Div::FINE - 1) / Div::FINE * Div::FINE;
     if (share < 1) share = 1;
     w.share = share;
     w.begin = share * blockIdx.x;
@@ -238,20 +250,21 @@ __device__ __forceinline__ AttnWalk<Div> attn_walk_start(const AttnParams& p, lo
             AttnSeq q;
             q.load(p, s, false);
             const int tiles = q.tiles(w.tt);
-            const long long c = q.before(tiles, w.tt, Div::ITEM) * p.num_kv_heads;
+            const long long c = q.before<Div>(tiles, w.tt, p.group_log2) * p.num_kv_heads;
             if (w.begin < pre + c) {
                 const long long o = w.begin - pre;
                 int lo = 0, hi = tiles - 1;  // the last tile that starts at or before o
                 while (lo < hi) {
                     const int mid = (lo + hi + 1) >> 1;
-                    if (q.before(mid, w.tt, Div::ITEM) * p.num_kv_heads <= o) lo = mid; else hi = mid - 1;
+                    if (q.before<Div>(mid, w.tt, p.group_log2) * p.num_kv_heads <= o) lo = mid; else hi = mid - 1;
                 }
-                const long long start = q.before(lo, w.tt, Div::ITEM) * p.num_kv_heads;
-                const int g = (int)((o - start) / (q.keys(lo, w.tt) + Div::ITEM));
+                const long long start = q.before<Div>(lo, w.tt, p.group_log2) * p.num_kv_heads;
+                const long long each_head = (long long)q.keys(lo, w.tt) * q.per_key<Div>(lo, w.tt, p.group_log2) + Div::ITEM;
+                const int g = (int)((o - start) / each_head);
                 scratch[NW + 1] = s;
                 scratch[NW + 2] = lo;
                 scratch[NW + 3] = g;
-                scratch[NW + 4] = pre + start + (long long)g * (q.keys(lo, w.tt) + Div::ITEM);
+                scratch[NW + 4] = pre + start + g * each_head;
                 break;
             }
             pre += c;
@@ -322,7 +335,7 @@ __device__ __forceinline__ bool attn_merge(const AttnParams& p, const AttnItem& 
     __threadfence();
     if (!sync()) return false;
     if (tid == 0) {
-        int* count = p.counters + Walk::owner(it.at, it.keys, share, 0) * 8;
+        int* count = p.counters + Walk::owner(it, share, 0) * 8;
         const int last = atomicAdd(count, 1) == it.nparts - 1;
         if (last) *count = 0;
         *flag = last;
@@ -346,7 +359,7 @@ __device__ __forceinline__ bool attn_merge(const AttnParams& p, const AttnItem& 
                 const int i = i0 + b;
                 ml[b] = make_float2(-INFINITY, 0.f);
                 if (i < it.nparts) {
-                    const int slot = attn_partial(Walk::owner(it.at, it.keys, share, i), i);
+                    const int slot = attn_partial(Walk::owner(it, share, i), i);
                     ml[b] = __ldcg(&p.ws_ml[(long long)slot * p.part_rows + r]);
                     const float4* o = p.ws_o + attn_partial_at(p, slot, D, 16 * c, r);
 #pragma unroll

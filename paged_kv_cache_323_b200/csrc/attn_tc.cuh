@@ -55,7 +55,8 @@ using tc::tc_fence_after;
 using tc::tc_fence_before;
 using tc::tma_load_5d;
 
-using TcDivision = AttnDivision<256, 128, 512, 192>;
+// A step of 128 keys takes a full tile 3300 clocks, an item 8000 to 12000 besides.
+using TcDivision = AttnDivision<256, 128, 2, 128, 512, 768>;
 
 // ------------------------------------------------------------ PTX wrappers
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int c0, int c1, int c2,
@@ -1028,7 +1029,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 const bool here = row < rows;
                 const bool split = u.nparts > 1, few = u.nparts <= FEW_PARTS;
                 const int slot = attn_partial(blockIdx.x, u.part);
-                int* count = split ? p.counters + AttnWalk<TcDivision>::owner(u.at, u.keys, walk0.share, 0) * 8 + (warp & 7)
+                int* count = split ? p.counters + AttnWalk<TcDivision>::owner(u, walk0.share, 0) * 8 + (warp & 7)
                                    : nullptr;
                 // A whole item: o / l.  Part of a split one: o, with its m and l.
                 w0 *= split ? vs : l == 0.f ? 0.f : vs / l;  // no key seen: a zero row
@@ -1165,7 +1166,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                                 if (i >= u.nparts || !here) continue;
                                 float2 ml = make_float2(m, l);
                                 if (i != u.part || written) {
-                                    const int si = attn_partial(AttnWalk<TcDivision>::owner(u.at, u.keys, walk0.share, i), i);
+                                    const int si = attn_partial(AttnWalk<TcDivision>::owner(u, walk0.share, i), i);
                                     ml = __ldcg(&p.ws_ml[(long long)si * p.part_rows + row]);
                                     from[i] = p.ws_o + attn_partial_at(p, si, D, 0, row);
                                 }
@@ -1363,7 +1364,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 for (int r = few ? first_row : 0; r < n; ++r)
                     p.ws_ml[(long long)attn_partial(blockIdx.x, u.part) * p.part_rows + r] = make_float2(-INFINITY, 0.f);
                 __threadfence();
-                int* c = p.counters + AttnWalk<TcDivision>::owner(u.at, u.keys, walk.share, 0) * 8 + warp;
+                int* c = p.counters + AttnWalk<TcDivision>::owner(u, walk.share, 0) * 8 + warp;
                 if (atomicAdd(c, 1) == u.nparts - 1) *c = 0;
             }
         }
