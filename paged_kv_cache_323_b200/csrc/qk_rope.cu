@@ -17,14 +17,18 @@ cudaError_t launch_inst(const RopeParams& p, bool interleaved, unsigned grid, cu
 
 cudaError_t launch_qk_rope(const RopeParams& p0, int dtype, bool fp8, bool interleaved, int D, cudaStream_t st) {
     RopeParams p = p0;
-    const int rows = p.num_heads + 2 * p.num_kv_heads;
-    const int rows_per_pass = kRopeThreads / (D * (dtype == PKV_F32 ? 4 : 2) / 16);
-    const int passes = (rows + rows_per_pass - 1) / rows_per_pass;
-    // few tokens: a token's heads over several CTAs, until every SM has one
-    p.head_splits = 1;
-    while (p.head_splits < passes && (long long)p.num_tokens * p.head_splits < 2 * kAttnSms) ++p.head_splits;
+    const int rows_per_pass = kRopeThreads / (D * (dtype == PKV_F32 ? 4 : 2) / 32);
+    // several tokens to a CTA while every SM has four CTAs; few tokens: q, k and v apart
+    // (their loads one behind the other are what such a call waits for), and a token's
+    // heads over several CTAs until every SM has one
     p.tokens_per_cta = 1;
-    const long long ctas = (long long)p.num_tokens * p.head_splits;
+    while (p.tokens_per_cta < kRopeMaxTokens && p.num_tokens >= 8 * kAttnSms * p.tokens_per_cta) p.tokens_per_cta *= 2;
+    p.kinds_apart = p.num_tokens <= 8 * kAttnSms;
+    const int passes = (p.tokens_per_cta * p.num_heads + rows_per_pass - 1) / rows_per_pass;
+    p.head_splits = 1;
+    while (p.head_splits < passes && (long long)p.num_tokens * p.head_splits < kAttnSms) ++p.head_splits;
+    const long long ctas = ((long long)p.num_tokens + p.tokens_per_cta - 1) / p.tokens_per_cta * p.head_splits *
+                           (p.kinds_apart ? 3 : 1);
     const unsigned grid = (unsigned)ctas;
     if (dtype == PKV_F32)
         return D == 64 ? launch_inst<float, 64, false>(p, interleaved, grid, st)

@@ -380,10 +380,46 @@ def kv_cache_append(k_cache, v_cache, k, v, slot_mapping, stream=None) -> None:
     _check(rc, "kv_cache_append")
 
 
+# The calls below are made several times a layer, on work of microseconds: their
+# checks take the short way first (one expression) and the long one, which
+# says what is wrong, only for tensors that do not pass it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _ptr(t: torch.Tensor, name: str, dtype, device, shape) -> int:
+    """As :func:`_dev`, shape always given."""
+    if (t.dtype is dtype and t.get_device() == device.index and t.shape == shape and t.is_contiguous()):
+        return t.data_ptr()
+    return _dev(t, name, dtype, device=device, shape=shape)
+
+
+def _call_stream(stream, device) -> int:
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device.index)
+    return _stream(stream, device)
+
+
+def _call(name: str, device, args) -> None:
+    if torch.cuda.current_device() == device.index:
+        rc = getattr(lib, name)(*args)
+    else:
+        with torch.cuda.device(device):
+            rc = getattr(lib, name)(*args)
+    if rc != PKV_OK:
+        raise PagedKVError(rc, name)
+
+
 def _rows(t: torch.Tensor, name: str, dtype, device, shape) -> tuple[int, int]:
     """(device pointer, elements between two tokens) of [tokens][heads][head_dim]
     rows: the heads of a token are contiguous, tokens may lie apart (a slice
     of a projection's output)."""
+    T, H, D = shape
+    if t.dtype is dtype and t.get_device() == device.index and t.shape == shape:
+        if t.is_contiguous():
+            return t.data_ptr(), H * D
+        s0, s1, s2 = t.stride()
+        if s2 == 1 and s1 == D and s0 >= H * D:
+            return t.data_ptr(), s0 if T > 1 else H * D
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.device != device:
@@ -392,7 +428,6 @@ def _rows(t: torch.Tensor, name: str, dtype, device, shape) -> tuple[int, int]:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    T, H, D = shape
     if t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     if T > 1 and t.stride(0) < H * D:
@@ -437,25 +472,25 @@ def _rope(name, q_out, q, k, v, k_cache, v_cache, scales, slot_mapping, position
     act = torch.bfloat16 if scales is not None else k_cache.dtype
     pool = torch.float8_e4m3fn if scales is not None else act
     want = (T,) if positions.dim() == 1 and len(sections) == 1 else (len(sections), T)
-    rows = [_rows(q_out, "q_out", act, dev, (T, H, D)), _rows(q, "q", act, dev, (T, H, D)),
-            _rows(k, "k", act, dev, (T, Hkv, D)), _rows(v, "v", act, dev, (T, Hkv, D))]
-    args = [r[0] for r in rows]
-    args += [_dev(k_cache, "k_cache", pool, device=dev), _dev(v_cache, "v_cache", pool, device=dev)]
+    (qo_p, qo_s), (q_p, q_s) = _rows(q_out, "q_out", act, dev, (T, H, D)), _rows(q, "q", act, dev, (T, H, D))
+    (k_p, k_s), (v_p, v_s) = _rows(k, "k", act, dev, (T, Hkv, D)), _rows(v, "v", act, dev, (T, Hkv, D))
+    pool_shape = (N, Hkv, bs, D)
+    args = [qo_p, q_p, k_p, v_p, _ptr(k_cache, "k_cache", pool, dev, pool_shape),
+            _ptr(v_cache, "v_cache", pool, dev, pool_shape)]
     if scales is not None:
-        args += [_dev(s, n, torch.float32, device=dev, shape=(Hkv,))
-                 for s, n in zip(scales, ("k_scales", "v_scales"))]
-    args += [_dev(slot_mapping, "slot_mapping", torch.int64, device=dev, shape=(T,)),
-             _dev(positions, "positions", torch.int32, device=dev, shape=want),
-             _dev(inv_freq, "inv_freq", torch.float32, device=dev, shape=(pairs,))]
-    args += [None if w is None else _dev(w, n, act, device=dev, shape=(D,))
-             for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight"))]
-    args += [float(eps), (ctypes.c_int * len(sections))(*sections), len(sections), int(bool(interleaved))]
-    args += [r[1] for r in rows] + [T, H, Hkv, D, bs, N]
+        args += [_ptr(scales[0], "k_scales", torch.float32, dev, (Hkv,)),
+                 _ptr(scales[1], "v_scales", torch.float32, dev, (Hkv,))]
+    args += [_ptr(slot_mapping, "slot_mapping", torch.int64, dev, (T,)),
+             _ptr(positions, "positions", torch.int32, dev, want),
+             _ptr(inv_freq, "inv_freq", torch.float32, dev, (pairs,)),
+             None if q_weight is None else _ptr(q_weight, "q_weight", act, dev, (D,)),
+             None if k_weight is None else _ptr(k_weight, "k_weight", act, dev, (D,)),
+             eps, (_I * len(sections))(*sections), len(sections), 1 if interleaved else 0,
+             qo_s, q_s, k_s, v_s, T, H, Hkv, D, bs, N]
     if scales is None:
         args.append(_dtype_code(q))
-    with torch.cuda.device(dev):
-        rc = getattr(lib, name)(*args, _stream(stream, dev))
-    _check(rc, name)
+    args.append(_call_stream(stream, dev))
+    _call(name, dev, args)
 
 
 def paged_attention_prefill_workspace_size(num_tokens: int, num_heads: int, num_kv_heads: int, head_dim: int,
@@ -495,7 +530,7 @@ def paged_attention_tree(out, q, k_cache, v_cache, block_tables, context_lens, q
     without the queries), itself and its ancestors.  parents int32 [T]: index
     of the parent among the sequence's drafts, below the draft's own, or -1."""
     _attend("paged_attention_tree", out, q, k_cache, v_cache, None, block_tables, context_lens, query_start,
-            parents, scale, num_blocks, workspace, stream)
+            parents, scale, num_blocks, workspace, stream, tree=True)
 
 
 def paged_attention_tree_fp8(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
@@ -503,11 +538,11 @@ def paged_attention_tree_fp8(out, q, k_cache, v_cache, k_scales, v_scales, block
                              workspace: torch.Tensor | None = None, stream=None) -> None:
     """The same over fp8 caches with per-kv-head float32 scales; q and out bf16."""
     _attend("paged_attention_tree_fp8", out, q, k_cache, v_cache, (k_scales, v_scales), block_tables,
-            context_lens, query_start, parents, scale, num_blocks, workspace, stream)
+            context_lens, query_start, parents, scale, num_blocks, workspace, stream, tree=True)
 
 
 def _attend(name, out, q, k_cache, v_cache, scales, block_tables, context_lens, query_start, parents, scale,
-            num_blocks, workspace, stream):
+            num_blocks, workspace, stream, tree=False):
     T, H, D = q.shape
     N, Hkv, bs, D2 = k_cache.shape
     if D2 != D or tuple(out.shape) != (T, H, D) or tuple(v_cache.shape) != tuple(k_cache.shape):
@@ -518,31 +553,42 @@ def _attend(name, out, q, k_cache, v_cache, scales, block_tables, context_lens, 
     act = torch.bfloat16 if scales is not None else k_cache.dtype
     pool = torch.float8_e4m3fn if scales is not None else act
     q_ptr, q_stride = _rows(q, "q", act, dev, (T, H, D))
-    args = [_dev(out, "out", act, device=dev), q_ptr, _dev(k_cache, "k_cache", pool, device=dev),
-            _dev(v_cache, "v_cache", pool, device=dev)]
+    pool_shape = (N, Hkv, bs, D)
+    args = [_ptr(out, "out", act, dev, (T, H, D)), q_ptr, _ptr(k_cache, "k_cache", pool, dev, pool_shape),
+            _ptr(v_cache, "v_cache", pool, dev, pool_shape)]
     if scales is not None:
-        args += [_dev(s, n, torch.float32, device=dev, shape=(Hkv,))
-                 for s, n in zip(scales, ("k_scales", "v_scales"))]
-    args += [_dev(block_tables, "block_tables", torch.int32, device=dev),
-             _dev(context_lens, "context_lens", torch.int32, device=dev),
-             _dev(query_start, "query_start", torch.int32, device=dev, shape=(B + 1,))]
-    if name.startswith("paged_attention_tree"):
-        args.append(_dev(parents, "parents", torch.int32, device=dev, shape=(T,)))
-    need = paged_attention_prefill_workspace_size(T, H, Hkv, D, _dtype_code(k_cache))
-    st = _stream(stream, dev)
-    if workspace is None and need > 0:
-        with torch.cuda.stream(_torch_stream(st, dev)):
-            if torch.cuda.is_current_stream_capturing():
+        args += [_ptr(scales[0], "k_scales", torch.float32, dev, (Hkv,)),
+                 _ptr(scales[1], "v_scales", torch.float32, dev, (Hkv,))]
+    args += [_ptr(block_tables, "block_tables", torch.int32, dev, (B, maxb)),
+             _ptr(context_lens, "context_lens", torch.int32, dev, (B,)),
+             _ptr(query_start, "query_start", torch.int32, dev, (B + 1,))]
+    if tree:
+        args.append(_ptr(parents, "parents", torch.int32, dev, (T,)))
+    st = _call_stream(stream, dev)
+    if workspace is None:
+        need = lib.paged_attention_prefill_workspace_size(T, H, Hkv, D, _dtype_code(k_cache))
+        workspace = _prefill_workspaces.get((dev.index, st))
+        if need > 0:
+            if _capturing(st, dev):
                 raise ValueError(f"{name}: pass a workspace to a call that is captured into a graph")
-        workspace = _workspace_for(need, dev, st, _prefill_workspaces)
-    ws_ptr = _dev(workspace, "workspace", torch.uint8, device=dev) if workspace is not None else None
-    ws_bytes = workspace.numel() if workspace is not None else 0
-    args += [q_stride, T, B, H, Hkv, D, bs, maxb, float(scale), N if num_blocks is None else int(num_blocks)]
+            if workspace is None or workspace.numel() < need:
+                workspace = _workspace_for(need, dev, st, _prefill_workspaces)
+        ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    else:
+        ws_ptr, ws_bytes = _dev(workspace, "workspace", torch.uint8, device=dev), workspace.numel()
+    args += [q_stride, T, B, H, Hkv, D, bs, maxb, scale, N if num_blocks is None else int(num_blocks)]
     if scales is None:
         args.append(_dtype_code(q))
-    with torch.cuda.device(dev):
-        rc = getattr(lib, name)(*args, ws_ptr, ws_bytes, st)
-    _check(rc, name)
+    args += [ws_ptr, ws_bytes, st]
+    _call(name, dev, args)
+
+
+def _capturing(stream_handle: int, dev: torch.device) -> bool:
+    if _raw_stream is not None and stream_handle == _raw_stream(dev.index) and \
+            dev.index == torch.cuda.current_device():
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(_torch_stream(stream_handle, dev)):
+        return torch.cuda.is_current_stream_capturing()
 
 
 def copy_blocks(k_cache, v_cache, src_dst_pairs, stream=None) -> None:

@@ -10,8 +10,21 @@ from test_binding_checks import Dev as HostDev, pk  # noqa: F401
 
 
 class Dev(HostDev):
-    def stride(self, i):
-        return self.t.stride(i)
+    def stride(self, *i):
+        return self.t.stride(*i)
+
+    def is_contiguous(self):
+        return self._contiguous and self.t.is_contiguous()
+
+    def get_device(self):
+        return self.device.index if self.is_cuda else -1
+
+
+@pytest.fixture(autouse=True)
+def no_stream(monkeypatch):
+    from paged_kv_cache_323_b200 import pagedkv
+
+    monkeypatch.setattr(pagedkv, "_raw_stream", lambda index: 0)
 
 
 def _attn(pk, name, **kw):
