@@ -19,20 +19,18 @@
 // stays in TMEM for the whole item.
 //
 // The reference m of a row's weights need not be its maximum, it cancels in
-// the quotient.  With bf16 weights, as wide in range as fp32, m is the largest
-// of the first 32 scores that the row sees, and no other maximum is taken: when
-// the sum has passed 2^40 after a step, m, the sum and O are moved by its
-// power of two (hardly ever).  f16 weights (fp8 caches) take the maximum of a
-// step first and move m when it is exceeded by 2^8.
+// the quotient, and bf16 weights are as wide in range as fp32: m is the largest
+// of the first 32 scores that the row sees, and no other maximum is taken.
+// When the sum has passed 2^40 after a step, m, the sum and O are moved by its
+// power of two (hardly ever).
 //
 // Warps: 0-3 and 4-7 softmax, 8 producer (TMA: one 5-D copy brings a whole
 // block of K or V in the layout the MMA wants), 9 MMA issue, 10 the walk;
-// fp8 caches: 12-15 widen each K and V tile to f16.  e4m3 values are exact in
-// f16, q is scaled per row by a power of two so that its bf16 values fit f16
-// (exact for all within 2^31 of the row's largest), and P is rounded to f16.
+// fp8 caches: 12-19 widen each K and V tile to
+// bf16, which holds every e4m3 value.
 //
-// Rounding: P to bf16 (f16 over fp8 caches) before the product with V, as the
-// tensor cores take it; sums, maxima and O are fp32.
+// Rounding: P to bf16 before the product with V, as the tensor cores take it;
+// sums and O are fp32.
 //
 // A masked key's weight is 0, and 0 * inf or 0 * nan would reach the row all
 // the same: rows whose result is not finite are computed again, key by key,
@@ -240,17 +238,11 @@ __device__ __forceinline__ void store_sector(void* to, const uint32_t (&r)[8]) {
                  : "memory");
 }
 
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 // Weights 2^(x q + m) of N scores of a row, packed for the MMA; sum gets their
 // total.  One pair in POLY_OF goes by ex2_poly, so that the special-function
 // unit (a quarter of the lanes a clock) and the FMA pipe share the work.
 constexpr int POLY_OF = 8;
-template <bool FP8, int N, bool POLY = true>
+template <int N, bool POLY = true>
 __device__ __forceinline__ void weights(const float* x, float2 q, float2 m, uint32_t* pk, float2& sum) {
     float2 sum1 = make_float2(0.f, 0.f);
 #pragma unroll
@@ -263,7 +255,7 @@ __device__ __forceinline__ void weights(const float* x, float2 q, float2 m, uint
             y.y = ex2(y.y);
         }
         if (c & 1) sum1 = add2(sum1, y); else sum = add2(sum, y);
-        pk[c] = FP8 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
+        pk[c] = pack_bf16(y.x, y.y);
     }
     sum = add2(sum, sum1);
 }
@@ -298,36 +290,33 @@ struct Cfg {
     static constexpr int NSLOT = FP8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);
     static constexpr int NRAW = FP8 ? (D == 128 ? 4 : 8) : 0;
     static constexpr int NLOAD = FP8 ? NRAW : NSLOT;  // slots that TMA fills
-    static constexpr int THREADS = FP8 ? 512 : 384;
+    static constexpr int WIDEN = FP8 ? 256 : 0;      // threads that widen
+    static constexpr int THREADS = 384 + WIDEN;
     static constexpr int ITEMS = FP8 ? 2 : 4;       // items the walk is ahead
     // registers: what the launch gives all threads, and its split among roles
-    static constexpr int REGS_SOFTMAX = FP8 ? 176 : 216;
+    static constexpr int REGS_SOFTMAX = FP8 ? 152 : 216;
     static constexpr int REGS_ISSUE = FP8 ? 64 : 72;
-    static constexpr int REGS_WIDEN = 96;
+    static constexpr int REGS_WIDEN = 56;
     static constexpr int REGS_LAUNCH = 65536 / THREADS / 8 * 8;
-    static_assert(256 * REGS_SOFTMAX + 128 * REGS_ISSUE + (FP8 ? 128 * REGS_WIDEN : 0) <= THREADS * REGS_LAUNCH,
+    static_assert(256 * REGS_SOFTMAX + 128 * REGS_ISSUE + WIDEN * REGS_WIDEN <= THREADS * REGS_LAUNCH,
                   "the roles' registers come out of the launch's");
-    // f16 weights are held 2^7 times larger: below 2^15, and a weight loses less than
-    // 2^-32 of the largest to f16's smallest step, 2^-24
-    static constexpr float SHIFT = 7.f;
     static constexpr uint32_t TMEM_COLS = 512;      // S / P of both pipelines, then O of both
     static constexpr uint32_t O_COL = 256;
-    static constexpr uint32_t FORMAT = FP8 ? 0u : 1u;  // f16 or bf16
-    static constexpr uint32_t IDESC_QK = tc::idesc_make(128, 128, FORMAT, false, false);
-    static constexpr uint32_t IDESC_PV = tc::idesc_make(128, D, FORMAT, false, true);
+    static constexpr uint32_t IDESC_QK = tc::idesc_bf16(128, 128, false, false);
+    static constexpr uint32_t IDESC_PV = tc::idesc_bf16(128, D, false, true);
 
     static constexpr int Q_OFF = 0;
     static constexpr int SLOT_OFF = 2 * QTILE;
     static constexpr int RAW_OFF = SLOT_OFF + NSLOT * TILE;
     static constexpr int BAR_OFF = RAW_OFF + NRAW * RAW;
-    // full/empty of the load ring, of the widened ring, q_full q_empty q_wide,
+    // full/empty of the load ring, of the widened ring, q_full q_empty,
     // s_full[2] p_full[2] p_rest[2] o_full[2], x_full x_empty, item full/empty, sync, mma_done
-    static constexpr int NBARS = 2 * NLOAD + (FP8 ? 2 * NSLOT : 0) + 3 + 8 + 2 + 2 * ITEMS + 2;
+    static constexpr int NBARS = 2 * NLOAD + (FP8 ? 2 * NSLOT : 0) + 2 + 8 + 2 + 2 * ITEMS + 2;
     static constexpr int LOAD_FULL = BAR_OFF, LOAD_EMPTY = LOAD_FULL + 8 * NLOAD;
     static constexpr int SLOT_FULL = FP8 ? LOAD_EMPTY + 8 * NLOAD : LOAD_FULL;  // what the MMA waits for
     static constexpr int SLOT_EMPTY = FP8 ? SLOT_FULL + 8 * NSLOT : LOAD_EMPTY;
-    static constexpr int Q_FULL = SLOT_EMPTY + 8 * NSLOT, Q_EMPTY = Q_FULL + 8, Q_WIDE = Q_FULL + 16;
-    static constexpr int S_FULL = Q_FULL + 24, P_FULL = S_FULL + 16, P_REST = S_FULL + 32, O_FULL = S_FULL + 48;
+    static constexpr int Q_FULL = SLOT_EMPTY + 8 * NSLOT, Q_EMPTY = Q_FULL + 8;
+    static constexpr int S_FULL = Q_FULL + 16, P_FULL = S_FULL + 16, P_REST = S_FULL + 32, O_FULL = S_FULL + 48;
     static constexpr int X_FULL = S_FULL + 64, X_EMPTY = X_FULL + 8;
     static constexpr int ITEM_FULL = X_EMPTY + 8, ITEM_EMPTY = ITEM_FULL + 8 * ITEMS;
     static constexpr int SYNC_BAR = ITEM_EMPTY + 8 * ITEMS, MMA_DONE = SYNC_BAR + 8;
@@ -336,8 +325,7 @@ struct Cfg {
     static constexpr int ITEM_OFF = (MISC_OFF + 48 + 15) / 16 * 16;
     static constexpr int WALK_OFF = ITEM_OFF + ITEMS * 64;
     static constexpr int ML_OFF = WALK_OFF + (THREADS / 32 + 8) * 8;  // float2[128]
-    static constexpr int QS_OFF = ML_OFF + 128 * 8;                    // 256 exponents, fp8
-    static constexpr int SMEM_BYTES = QS_OFF + (FP8 ? 256 : 0) + 1024;
+    static constexpr int SMEM_BYTES = ML_OFF + 128 * 8 + 1024;
     static_assert(SMEM_BYTES <= 232448, "227 KB of shared memory");
     static_assert(sizeof(AttnItem) <= 64, "");
 };
@@ -486,24 +474,22 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     int* merge_flag = reinterpret_cast<int*>(smem + C::MISC_OFF + 8);
     int* turns = reinterpret_cast<int*>(smem + C::MISC_OFF + 16);  // [8] split items each softmax warp has counted
     float2* ml_x = reinterpret_cast<float2*>(smem + C::ML_OFF);
-    unsigned char* q_row_scale = smem + C::QS_OFF;  // biased exponents
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         auto init = [&](int off, uint32_t count) { mbar_init(reinterpret_cast<uint64_t*>(smem + off), count); };
         for (int i = 0; i < C::NLOAD; ++i) {
             init(C::LOAD_FULL + 8 * i, 1);
-            init(C::LOAD_EMPTY + 8 * i, FP8 ? 4 : 1);
+            init(C::LOAD_EMPTY + 8 * i, FP8 ? C::WIDEN / 32 : 1);
         }
         if constexpr (FP8) {
             for (int i = 0; i < C::NSLOT; ++i) {
-                init(C::SLOT_FULL + 8 * i, 4);
+                init(C::SLOT_FULL + 8 * i, C::WIDEN / 32);
                 init(C::SLOT_EMPTY + 8 * i, 1);
             }
         }
         init(C::Q_FULL, 1);
-        init(C::Q_EMPTY, FP8 ? 9 : 1);  // the last QK^T, fp8: and the softmax warps have the rows' scales
-        init(C::Q_WIDE, 4);
+        init(C::Q_EMPTY, 1);
         for (int i = 0; i < 2; ++i) {
             init(C::S_FULL + 8 * i, 1);
             init(C::P_FULL + 8 * i, 4);
@@ -514,7 +500,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
         init(C::X_EMPTY, 4);
         for (int i = 0; i < C::ITEMS; ++i) {
             init(C::ITEM_FULL + 8 * i, 1);
-            init(C::ITEM_EMPTY + 8 * i, 10 + (FP8 ? 4 : 0));  // producer, MMA, softmax and widening warps
+            init(C::ITEM_EMPTY + 8 * i, 10 + C::WIDEN / 32);  // producer, MMA, softmax and widening warps
         }
         init(C::SYNC_BAR, 8);
         init(C::MMA_DONE, 1);
@@ -652,8 +638,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                            v_desc = sw128_desc(sb + C::SLOT_OFF, C::HSTEP, C::GSTRIDE);
             const uint32_t q_lo = (uint32_t)q_desc, q_hi = (uint32_t)(q_desc >> 32), k_lo = (uint32_t)k_desc,
                            k_hi = (uint32_t)(k_desc >> 32), v_lo = (uint32_t)v_desc, v_hi = (uint32_t)(v_desc >> 32);
-            // a negative scale turns the order of the scores: they are taken with A negated
-            const uint32_t idesc_qk = C::IDESC_QK | (p.qscale < 0.f ? 1u << 13 : 0u);
+            uint32_t idesc_qk = 0;
             uint32_t slot = 0, slot_phase = 0;  // loads are used in their order
             uint32_t q_phase = 0, p_phase0 = 0, p_phase1 = 0;
             bool ok = true;
@@ -694,7 +679,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 if (plan.steps == 0) continue;
                 const bool wide = plan.wide;
                 const int n0 = plan.n0, n1 = plan.n1;
-                if (!(ok = wait(FP8 ? C::Q_WIDE : C::Q_FULL, q_phase))) break;
+                // a negative scale turns the order of the scores: they are taken with A negated
+                idesc_qk = C::IDESC_QK | ((FP8 ? p.qscale * p.k_scales[u.g] : p.qscale) < 0.f ? 1u << 13 : 0u);
+                if (!(ok = wait(C::Q_FULL, q_phase))) break;
                 q_phase ^= 1;
                 mma_any = true;
                 int left = plan.steps;  // K tiles not used up yet
@@ -770,7 +757,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
         const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t t_s = t_lane + wg * 128, t_o = t_lane + C::O_COL + wg * 128;
         int base = 0;                  // loads of the items before
-        uint32_t s_phase = 0, o_phase[2] = {0, 0}, x_phase = 0, sync_phase = 0, q_phase = 0;
+        uint32_t s_phase = 0, o_phase[2] = {0, 0}, x_phase = 0, sync_phase = 0;
         bool x_pending = false;        // WG 1: its O has not been read yet
         bool ok = true;
         auto sync = [&]() -> bool {    // all 256 threads
@@ -799,15 +786,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             const int tok = (row >> gl) < u.ntok ? row >> gl : u.ntok - 1;
             const int qi = u.pos - u.first + tok;  // index in its sequence
             float qs = p.qscale;
-            if constexpr (FP8) {
-                qs *= p.k_scales[u.g];
-                if (plan.steps > 0) {
-                    if (!(ok = wait(C::Q_WIDE, q_phase))) break;
-                    q_phase ^= 1;
-                    qs *= __uint_as_float((uint32_t)q_row_scale[row] << 23);
-                    arrive(C::Q_EMPTY);
-                }
-            }
+            if constexpr (FP8) qs *= p.k_scales[u.g];
             // (a negative scale: the scores come negated.)  A scale of 0 weighs what is
             // seen alike, and -inf * 0 is not -inf
             const float qa = fmaxf(fabsf(qs), __uint_as_float(1u));
@@ -874,27 +853,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) x[e] = word & (1u << e) ? x[e] : -INFINITY;
                 };
-                if constexpr (FP8) {
-                    // f16 weights: the maximum first
-                    float mx = -INFINITY;
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        float x[32];
-                        tmem_ld32(t_s + 32 * c, x);
-                        tmem_wait_ld();
-                        if (__builtin_expect(masked, 0)) mask32(x, c == 0 ? w[0] : c == 1 ? w[1] : c == 2 ? w[2] : w[3]);
-                        mx = largest32(x, mx);
-                    }
-                    mx *= qa;
-                    if (__any_sync(0xffffffffu, !(mx <= m + (8.f + C::SHIFT)))) {
-                        if (!(mx < INFINITY)) l = __uint_as_float(0x7fffffffu);  // for slow_row
-                        const float mn = fmaxf(m, mx - C::SHIFT);
-                        const float alpha = mn == -INFINITY ? 1.f : ex2(m - mn);
-                        m = mn;
-                        l *= alpha;
-                        if (t > 0) rescale_o(alpha);
-                    }
-                } else if (stale) {
+                if (stale) {
                     rescale_o(alpha_next);
                     stale = false;
                 }
@@ -912,12 +871,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                             tmem_wait_ld();
                             if (!__all_sync(0xffffffffu, word == 0xffffffffu)) mask32(x, word);
                             // the first keys that a row sees give its reference
-                            if (!FP8 && __any_sync(0xffffffffu, m == -INFINITY)) {
+                            if (__any_sync(0xffffffffu, m == -INFINITY)) {
                                 const float mx = largest32(x, -INFINITY) * qa;
                                 m = m == -INFINITY ? mx : m;
                             }
                             const float mm = m == -INFINITY ? 0.f : -m;
-                            weights<FP8, 32, false>(x, q2, make_float2(mm, mm), pk, sum);  // exactly 0 where masked
+                            weights<32, false>(x, q2, make_float2(mm, mm), pk, sum);  // exactly 0 where masked
                         } else {
 #pragma unroll
                             for (int e = 0; e < 16; ++e) pk[e] = 0u;
@@ -931,25 +890,38 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                         }
                     }
                 } else {
-                    float x[128];
-                    uint32_t pk[48];
+                    // (with the registers of the fp8 kernel, 64 keys at a time)
+                    constexpr int AT_ONCE = FP8 ? 64 : 128;
+                    float x[AT_ONCE];
+                    uint32_t pk[AT_ONCE == 128 ? 48 : 32];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, x + 32 * c);
+                    for (int c = 0; c < AT_ONCE / 32; ++c) tmem_ld32(t_s + 32 * c, x + 32 * c);
                     tmem_wait_ld();
                     if (t == 0) {
-                        if (!FP8) m = largest32(x, -INFINITY) * qa;  // the row's reference
+                        m = largest32(x, -INFINITY) * qa;  // the row's reference
                         if (!(ok = o_readable())) break;
                     }
                     const float2 m2 = make_float2(-m, -m);
+                    if constexpr (AT_ONCE == 128) {
 #pragma unroll
-                    for (int c = 0; c < 3; ++c) weights<FP8, 32>(x + 32 * c, q2, m2, pk + 16 * c, sum);
-                    tmem_st32(t_s, pk);
-                    tmem_st16(t_s + 32, pk + 32);
+                        for (int c = 0; c < 3; ++c) weights<32>(x + 32 * c, q2, m2, pk + 16 * c, sum);
+                        tmem_st32(t_s, pk);
+                        tmem_st16(t_s + 32, pk + 32);
+                    } else {
+                        weights<32>(x, q2, m2, pk, sum);
+                        weights<32>(x + 32, q2, m2, pk + 16, sum);
+                        tmem_ld32(t_s + 64, x);
+                        tmem_ld32(t_s + 96, x + 32);
+                        tmem_st32(t_s, pk);
+                        tmem_wait_ld();
+                        weights<32>(x, q2, m2, pk, sum);
+                        tmem_st16(t_s + 32, pk);
+                    }
                     tmem_wait_st();
                     // the product of the first 96 keys may start
                     tc_fence_before();
                     arrive(C::P_FULL + 8 * wg);
-                    weights<FP8, 32>(x + 96, q2, m2, pk, sum);
+                    weights<32>(x + AT_ONCE - 32, q2, m2, pk, sum);
                     tmem_st16(t_s + 48, pk);
                 }
                 if (!ok) break;
@@ -957,17 +929,15 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 tc_fence_before();
                 arrive(C::P_REST + 8 * wg);
                 l += sum.x + sum.y;
-                if constexpr (!FP8) {
-                    if (__any_sync(0xffffffffu, !(l <= 0x1p40f))) {
-                        // NaN, infinite, or past what a weight can hold: for slow_row
-                        if (!(l <= 0x1p100f)) l = __uint_as_float(0x7fffffffu);
-                        if (t + 1 < nt) {
-                            const uint32_t e = l > 1.f ? (__float_as_uint(l) >> 23) - 127 : 0;  // l in [2^e, 2^(e + 1))
-                            alpha_next = __uint_as_float((127 - e) << 23);
-                            m += (float)e;
-                            l *= alpha_next;
-                            stale = true;  // O: once this step's product is complete
-                        }
+                if (__any_sync(0xffffffffu, !(l <= 0x1p40f))) {
+                    // NaN, infinite, or past what a weight can hold: for slow_row
+                    if (!(l <= 0x1p100f)) l = __uint_as_float(0x7fffffffu);
+                    if (t + 1 < nt) {
+                        const uint32_t e = l > 1.f ? (__float_as_uint(l) >> 23) - 127 : 0;  // l in [2^e, 2^(e + 1))
+                        alpha_next = __uint_as_float((127 - e) << 23);
+                        m += (float)e;
+                        l *= alpha_next;
+                        stale = true;  // O: once this step's product is complete
                     }
                 }
             }
@@ -1060,7 +1030,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 auto odd_rows = [&]() {
                     return __ballot_sync(0xffffffffu, here && nt > 0 && !(odd.x + odd.y == 0.f && l == l));
                 };
-                if (!split) {
+                if (rows_left <= 0) {
+                    // no rows of this warp
+                } else if (!split) {
 #pragma unroll 1
                     for (int c = 0; c < D; c += 32) {
                         float o[32];
@@ -1081,7 +1053,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                         for (int e = 0; e < D / 32; ++e)
                             to[lane * (D / 32) + e] = __float2bfloat16_rn(ls == 0.f ? 0.f : acc[e] / ls);
                     }
-                } else if (rows_left > 0) {
+                } else {
                     // With few parts each warp joins its own rows: the last of an item's parts to
                     // come has the others' results at hand and needs not write its own.
 #pragma unroll 1
@@ -1206,8 +1178,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
         // ----------------------------------------------------------- widening
         if constexpr (FP8) {
             regs_dec<C::REGS_WIDEN>();
-            const int t128 = tid - 384;
-            uint32_t rs = 0, raw_phase = 0, st = 0, empty_phase = 1, q_phase = 0;
+            const int tw = tid - 384;
+            uint32_t rs = 0, raw_phase = 0, st = 0, empty_phase = 1;
             bool ok = true;
             AttnItem u;
             for (int n = 0; ok && take_item(n, u); ++n) {
@@ -1215,53 +1187,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 plan.set(u, gl);
                 if (plan.steps == 0) continue;
                 const int32_t* bt = p.block_tables + (long long)u.seq * p.max_blocks_per_seq;
-                // q: bf16 -> f16 in place, each row times a power of two that brings
-                // its largest value to [2^14, 2^15)
-                if (!(ok = wait(C::Q_FULL, q_phase))) break;
-                q_phase ^= 1;
-                for (int t = 0; t < (plan.wide ? 2 : 1); ++t) {
-                    unsigned char* qr = smem + C::Q_OFF + t * C::QTILE + t128 * 128;
-                    uint32_t top = 0;
-#pragma unroll
-                    for (int h = 0; h < C::HALVES; ++h)
-#pragma unroll
-                        for (int c0 = 0; c0 < 8; ++c0) {
-                            const int c = c0 ^ (t128 & 7);  // neighbouring rows: other banks
-                            const uint4 w = *reinterpret_cast<const uint4*>(qr + h * C::QHALF + c * 16);
-                            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const uint32_t lo = (x[e] & 0x7fffu) << 16, hi = x[e] & 0x7fff0000u;
-                                top = top > lo ? top : lo;
-                                top = top > hi ? top : hi;
-                            }
-                        }
-                    // exponent of the largest |q| (as bits, they order like integers); infinities
-                    // and NaN stay what they are under any scale
-                    int ex = (int)(top >> 23);
-                    ex = ex == 0 ? 127 + 14 : ex > 254 ? 254 : ex;
-                    int up = 127 + 14 - ex + 127;  // biased exponent of the scale
-                    up = up < 1 ? 1 : up > 253 ? 253 : up;
-                    const float f = __uint_as_float((uint32_t)up << 23);
-                    q_row_scale[t * 128 + t128] = (unsigned char)(254 - up);
-#pragma unroll
-                    for (int h = 0; h < C::HALVES; ++h)
-#pragma unroll
-                        for (int c0 = 0; c0 < 8; ++c0) {
-                            const int c = c0 ^ (t128 & 7);
-                            uint4* at = reinterpret_cast<uint4*>(qr + h * C::QHALF + c * 16);
-                            const uint4 w = *at;
-                            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-                            uint32_t y[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                y[e] = pack_f16(__uint_as_float(x[e] << 16) * f,
-                                                __uint_as_float(x[e] & 0xffff0000u) * f);
-                            *at = make_uint4(y[0], y[1], y[2], y[3]);
-                        }
-                }
-                fence_proxy_async_smem();
-                arrive(C::Q_WIDE);
                 for (int lo = 0; lo < 2 * plan.steps; ++lo) {
                     bool v;
                     const int k0 = u.kv0 + plan.load_step(lo, v) * C::KEYS;
@@ -1277,8 +1202,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     unsigned char* wide = smem + C::SLOT_OFF + st * C::TILE;
                     constexpr int CPR = D / 16;  // 16-byte chunks of a raw row
 #pragma unroll
-                    for (int i = 0; i < C::KEYS * CPR / 128; ++i) {
-                        const int x = t128 + 128 * i, r = x / CPR, c = x % CPR;
+                    for (int i = 0; i < C::KEYS * CPR / C::WIDEN; ++i) {
+                        const int x = tw + C::WIDEN * i, r = x / CPR, c = x % CPR;
                         uint4 w = *reinterpret_cast<const uint4*>(raw + x * 16);
                         if (short_step) {
                             const uint32_t word = r < 32 ? there[0] : r < 64 ? there[1] : r < 96 ? there[2] : there[3];
@@ -1288,10 +1213,16 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                         uint32_t y[8];
 #pragma unroll
                         for (int e2 = 0; e2 < 4; ++e2) {
+                            uint32_t h[2];  // f16 pairs
                             asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
                                 "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-                                : "=r"(y[2 * e2]), "=r"(y[2 * e2 + 1])
+                                : "=r"(h[0]), "=r"(h[1])
                                 : "r"(in[e2]));
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
+                                y[2 * e2 + k] = pack_bf16(f.x, f.y);
+                            }
                         }
                         unsigned char* to = wide + (r >> 3) * C::GSTRIDE + (c >> 2) * C::HSTEP + (r & 7) * 128;
                         // lanes of the second half store their chunks in the other order: no bank conflicts

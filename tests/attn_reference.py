@@ -95,10 +95,7 @@ def attend(b: Batch, tree=False, lost=()):
     (head_dim additions of |q||k|, each within 2^-24) and moving every weight by
     that much; exponentials within 2^-12 relative where they are rounded to
     bf16 next, 2^-21 else; sums of n weights within n 2^-24 (pairwise and
-    blocked ones are far below).  Weights over fp8 caches are f16 with the
-    largest at 2^7 or above: below f16's normal range half a step, 2^-25, is
-    2^-32 of the largest, hence of their sum, so each value of v moves the row by
-    2^-32 |v| at most."""
+    blocked ones are far below)."""
     H, G, D, bs = b.H, b.G, b.D, b.bs
     ref = torch.zeros(b.T, H, D, dtype=torch.float64, device="cuda")
     bound = torch.zeros_like(ref)
@@ -149,9 +146,7 @@ def attend(b: Batch, tree=False, lost=()):
                 rel = 2 * (D * u * mag[:, None] + c * u + (2.0 ** -12 if narrow else 2.0 ** -21)) \
                     + (2.0 ** -8 if narrow else 0.0)
                 ref[r0:r0 + n, h] = o
-                if b.dtype == "fp8":
-                    bound[r0:r0 + n, h] = 2.0 ** -32 * (seen.double() @ vz.abs())
-                bound[r0:r0 + n, h] += rel * a + (2.0 ** -8 if narrow else u) * (o.abs() + rel * a)
+                bound[r0:r0 + n, h] = rel * a + (2.0 ** -8 if narrow else u) * (o.abs() + rel * a)
     return ref, bound + 1e-30
 
 

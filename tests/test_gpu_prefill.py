@@ -86,6 +86,16 @@ def test_scales(pk, dtype, scale):
     check(pk, b, False)
 
 
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+def test_negative_cache_scales(pk, sign):
+    """A kv head whose k scale is negative, under either sign of the softmax scale."""
+    b = Batch([(40, 300), (130, 130)], dtype="fp8", heads=8, kv_heads=2, seed=5)
+    b.ks[1] *= -1
+    b.vs[0] *= -1
+    b.scale *= sign
+    check(pk, b, False)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_large_scores(pk, dtype):
     """Scores of several hundred: the maximum moves, old sums are scaled down."""
