@@ -58,18 +58,18 @@ struct AttnParams {
 };
 
 // ------------------------------------------------------------ the division
-// ROWS: rows of a tile.  Work is counted in the time that one key takes a tile
-// of at most HALF rows; a larger tile takes TWICE of it.  An item whose share
-// of a CTA is at least COARSE keys is cut at multiples of FINE keys (balance),
-// in smaller calls items are cut at multiples of COARSE only (a part shorter
-// than that costs more in its merge than it saves).  ITEM: work of an item
-// besides its keys.
-template <int ROWS_, int HALF_, int TWICE_, int FINE_, int COARSE_, int ITEM_>
+// ROWS: rows of a tile.  A key is LESS work for a tile of at most HALF rows
+// and MORE for a larger one.  An item whose share of a CTA is at least COARSE
+// keys is cut at multiples of FINE keys (balance), in smaller calls items are
+// cut at multiples of COARSE only (a part shorter than that costs more in its
+// merge than it saves).  ITEM: work of an item besides its keys.
+template <int ROWS_, int HALF_, int LESS_, int MORE_, int FINE_, int COARSE_, int ITEM_>
 struct AttnDivision {
-    static constexpr int ROWS = ROWS_, HALF = HALF_, TWICE = TWICE_, FINE = FINE_, COARSE = COARSE_, ITEM = ITEM_;
+    static constexpr int ROWS = ROWS_, HALF = HALF_, LESS = LESS_, MORE = MORE_, FINE = FINE_, COARSE = COARSE_,
+                         ITEM = ITEM_;
     static_assert(COARSE % FINE == 0 && (FINE & (FINE - 1)) == 0 && (COARSE & (COARSE - 1)) == 0, "");
-    static constexpr int FULL = ROWS > HALF ? TWICE : 1;  // work per key of a full tile
-    __host__ __device__ static constexpr int per_key(int rows) { return rows > HALF ? TWICE : 1; }
+    static constexpr int FULL = ROWS > HALF ? MORE : LESS;  // work per key of a full tile
+    __host__ __device__ static constexpr int per_key(int rows) { return rows > HALF ? MORE : LESS; }
 };
 
 // Sequence s of a launch: its rows, and what its tiles cost.
@@ -265,6 +265,9 @@ __device__ __forceinline__ AttnWalk<Div> attn_walk_start(const AttnParams& p, lo
                 scratch[NW + 2] = lo;
                 scratch[NW + 3] = g;
                 scratch[NW + 4] = pre + start + g * each_head;
+                scratch[NW + 5] = q.q0;
+                scratch[NW + 6] = q.n;
+                scratch[NW + 7] = q.valid ? q.first : -1;
                 break;
             }
             pre += c;
@@ -280,7 +283,10 @@ __device__ __forceinline__ AttnWalk<Div> attn_walk_start(const AttnParams& p, lo
     w.t = (int)scratch[NW + 2];
     w.g = (int)scratch[NW + 3];
     w.at = scratch[NW + 4];
-    w.q.load(p, w.s, false);
+    w.q.q0 = (int)scratch[NW + 5];
+    w.q.n = (int)scratch[NW + 6];
+    w.q.valid = scratch[NW + 7] >= 0;
+    w.q.first = w.q.valid ? (int)scratch[NW + 7] : 0;
     return w;
 }
 

@@ -22,7 +22,7 @@ namespace pkv {
 
 // A 64-key step takes some 5 us: one step is worth a part of its own in calls
 // that do not fill the SMs otherwise.
-using SimtDivision = AttnDivision<64, 64, 1, 64, 64, 16>;
+using SimtDivision = AttnDivision<64, 64, 1, 1, 64, 64, 16>;
 
 template <int D>
 struct SimtCfg {

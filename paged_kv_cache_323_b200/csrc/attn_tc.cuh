@@ -54,8 +54,9 @@ using tc::tc_fence_after;
 using tc::tc_fence_before;
 using tc::tma_load_5d;
 
-// A step of 128 keys takes a full tile 3300 clocks, an item 8000 to 12000 besides.
-using TcDivision = AttnDivision<256, 128, 2, 128, 512, 768>;
+// A step of 128 keys takes a full tile 3300 clocks; a tile of at most 128 rows, two steps
+// at a time, 2150 where K and V come from HBM; an item takes some 10000 besides.
+using TcDivision = AttnDivision<256, 128, 2, 3, 128, 512, 1152>;
 
 // ------------------------------------------------------------ PTX wrappers
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int c0, int c1, int c2,
@@ -476,38 +477,24 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     float2* ml_x = reinterpret_cast<float2*>(smem + C::ML_OFF);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (tid == 0) {
-        auto init = [&](int off, uint32_t count) { mbar_init(reinterpret_cast<uint64_t*>(smem + off), count); };
-        for (int i = 0; i < C::NLOAD; ++i) {
-            init(C::LOAD_FULL + 8 * i, 1);
-            init(C::LOAD_EMPTY + 8 * i, FP8 ? C::WIDEN / 32 : 1);
-        }
-        if constexpr (FP8) {
-            for (int i = 0; i < C::NSLOT; ++i) {
-                init(C::SLOT_FULL + 8 * i, C::WIDEN / 32);
-                init(C::SLOT_EMPTY + 8 * i, 1);
-            }
-        }
-        init(C::Q_FULL, 1);
-        init(C::Q_EMPTY, 1);
-        for (int i = 0; i < 2; ++i) {
-            init(C::S_FULL + 8 * i, 1);
-            init(C::P_FULL + 8 * i, 4);
-            init(C::P_REST + 8 * i, 4);
-            init(C::O_FULL + 8 * i, 1);
-        }
-        init(C::X_FULL, 4);
-        init(C::X_EMPTY, 4);
-        for (int i = 0; i < C::ITEMS; ++i) {
-            init(C::ITEM_FULL + 8 * i, 1);
-            init(C::ITEM_EMPTY + 8 * i, 10 + C::WIDEN / 32);  // producer, MMA, softmax and widening warps
-        }
-        init(C::SYNC_BAR, 8);
-        init(C::MMA_DONE, 1);
-        *abort_flag = 0;
-        for (int i = 0; i < 8; ++i) turns[i] = 0;
-        fence_mbarrier_init();
+    for (int i = tid; i < C::NBARS; i += C::THREADS) {
+        const int off = C::BAR_OFF + 8 * i;
+        int count = 1;
+        if (off >= C::LOAD_EMPTY && off < C::LOAD_EMPTY + 8 * C::NLOAD && FP8) count = C::WIDEN / 32;
+        if (FP8 && off >= C::SLOT_FULL && off < C::SLOT_FULL + 8 * C::NSLOT) count = C::WIDEN / 32;
+        if (off >= C::P_FULL && off < C::O_FULL) count = 4;    // P_FULL, P_REST: a pipeline's softmax warps
+        if (off == C::X_FULL || off == C::X_EMPTY) count = 4;  // those of one pipeline
+        if (off >= C::ITEM_EMPTY && off < C::SYNC_BAR) count = 10 + C::WIDEN / 32;  // all warps that read items
+        if (off == C::SYNC_BAR) count = 8;                     // all softmax warps
+        mbar_init(reinterpret_cast<uint64_t*>(smem + off), count);
     }
+    if (tid < 8) turns[tid] = 0;
+    if (tid == 0) {
+        *abort_flag = 0;
+        for (const CUtensorMap* m : {&tmq, &tmk, &tmv})
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+    }
+    fence_mbarrier_init();
     if (warp == 9) {
         tc::tmem_alloc(tmem_slot, C::TMEM_COLS);
         tc::tmem_relinquish();
@@ -1056,31 +1043,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 } else {
                     // With few parts each warp joins its own rows: the last of an item's parts to
                     // come has the others' results at hand and needs not write its own.
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        float o[32];
-                        own(c, o);
-                        look(o);
-                    }
-                    uint32_t again = odd_rows();
-                    int seen = 0;
-                    if (few && lane == 0) asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(seen) : "l"(count) : "memory");
-                    seen = __shfl_sync(0xffffffffu, seen, 0);
-                    bool last = few && seen == u.nparts - 1;
-                    const bool written = !last || again != 0;
-                    if (written) {
-#pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            float o[32];
-                            own(c, o);
-                            if (here) {
-#pragma unroll
-                                for (int e = 0; e < 32; e += 4)
-                                    p.ws_o[attn_partial_at(p, slot, D, c + e, row)] =
-                                        make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                            }
-                        }
-                        if (here) p.ws_ml[(long long)slot * p.part_rows + row] = make_float2(m, l);
+                    float4* to = p.ws_o + attn_partial_at(p, slot, D, 0, row);
+                    float2* to_ml = p.ws_ml + (long long)slot * p.part_rows + row;
+                    auto redo = [&](uint32_t again) {  // rows of this part again, into the workspace
                         __syncwarp();
                         while (again) {
                             const int r = row0 + __ffs(again) - 1;
@@ -1093,6 +1058,29 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                                     [(lane * (D / 32)) % 4 + e] = acc[e];
                             if (lane == 0) p.ws_ml[(long long)slot * p.part_rows + r] = make_float2(ms, ls);
                         }
+                        __syncwarp();
+                    };
+                    int seen = 0;
+                    if (few && lane == 0) asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(seen) : "l"(count) : "memory");
+                    seen = __shfl_sync(0xffffffffu, seen, 0);
+                    bool last = few && seen == u.nparts - 1;
+                    bool from_ws = !last;  // this row's own part
+                    if (!last) {
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            float o[32];
+                            own(c, o);
+                            look(o);
+                            if (here) {
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    to[(c / 4 + e) * (long long)p.part_rows] =
+                                        make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                            }
+                        }
+                        if (here) *to_ml = make_float2(m, l);
+                        const uint32_t again = odd_rows();
+                        if (again) redo(again);
                     }
                     if (few) {
                         if (!last) {
@@ -1105,12 +1093,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                             if (last) *count = 0;
                             turns[warp] += 1;
                         }
-                        if (last) {
-                            __threadfence();
-                            // M = max m_i, out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i, in the parts' order
-                            float wi[FEW_PARTS], M = -INFINITY, L = 0.f;
+                        if (last) __threadfence();
+                        // M = max m_i, out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i, in the parts' order
+                        while (last) {
+                            float wi[FEW_PARTS], li[FEW_PARTS], M = -INFINITY, L = 0.f;
                             const float4* from[FEW_PARTS];
-                            float li[FEW_PARTS];
 #pragma unroll
                             for (int i = 0; i < FEW_PARTS; ++i) {
                                 wi[i] = -INFINITY;
@@ -1118,7 +1105,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                                 from[i] = nullptr;
                                 if (i >= u.nparts || !here) continue;
                                 float2 ml = make_float2(m, l);
-                                if (i != u.part || written) {
+                                if (i != u.part || from_ws) {
                                     const int si = attn_partial(AttnWalk<TcDivision>::owner(u, walk0.share, i), i);
                                     ml = __ldcg(&p.ws_ml[(long long)si * p.part_rows + row]);
                                     from[i] = p.ws_o + attn_partial_at(p, si, D, 0, row);
@@ -1138,6 +1125,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                             for (int c = 0; c < D; c += 32) {
                                 float o[32], x[32];
                                 own(c, x);
+                                look(x);
 #pragma unroll
                                 for (int e = 0; e < 32; ++e) o[e] = 0.f;
 #pragma unroll
@@ -1161,6 +1149,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                                 for (int e = 0; e < 32; ++e) o[e] *= inv;
                                 if (here) store32(dst + c, o);
                             }
+                            // rows of this part, not written so far, that are not finite: once more
+                            const bool mine = !from_ws && nt > 0 && here && !(odd.x + odd.y == 0.f && l == l);
+                            const uint32_t again = __ballot_sync(0xffffffffu, mine);
+                            if (again == 0) break;
+                            redo(again);
+                            from_ws = from_ws || mine;
                         }
                     }
                 }
