@@ -6,27 +6,30 @@
 // over the keys row r sees, with the running maximum m and sum of a softmax in
 // one pass over the keys.
 //
-// A CTA of 256 threads (a 16 x 16 grid) takes items of 64 rows in 64-key
-// steps.  Q, K and V are staged in shared memory; a thread
-// holds a 4 x 4 piece of the scores (rows 4 ty + i, keys tx + 16 j) and a
-// 4 x D/16 piece of the output.  Per 4 dims of the head it reads 4 + 4 float4
-// for 64 FMAs, which puts the kernel near what shared memory can feed; padded
-// rows keep those reads free of bank conflicts.  The scores go from one
-// thread to the others of its row through K's space, so two CTAs fit an SM
-// and one's loads overlap the other's products.
+// A CTA of 256 threads (a 16 x 16 grid) takes items of ROWS = 64 rows in 64-key
+// steps, or of 16 rows in calls of few rows a sequence.  Q, K and V are staged
+// in shared memory; a thread holds an R x 4 piece of the scores (rows R ty + i,
+// keys tx + 16 j; R = ROWS / 16) and an R x D/16 piece of the output.  Per 4
+// dims of the head it reads R + 4 float4 for 16 R FMAs, which with R = 4 puts
+// the kernel near what shared memory can feed; padded rows keep those reads
+// free of bank conflicts.  The scores go from one thread to the others of its
+// row through K's space, so two CTAs fit an SM and one's loads overlap the
+// other's products.
 #pragma once
 
 #include "attn_common.cuh"
 
 namespace pkv {
 
-// A 64-key step takes some 5 us: one step is worth a part of its own in calls
-// that do not fill the SMs otherwise.
-using SimtDivision = AttnDivision<64, 64, 1, 1, 64, 64, 16>;
+// A 64-key step is long enough to be a part of its own in calls that do not
+// fill the SMs otherwise.
+template <int ROWS>
+using SimtDivision = AttnDivision<ROWS, ROWS, 1, 1, 64, 64, 16>;
 
-template <int D>
+template <int D, int ROWS_>
 struct SimtCfg {
-    static constexpr int ROWS = SimtDivision::ROWS, KEYS = 64, THREADS = 256;
+    static constexpr int ROWS = ROWS_, KEYS = 64, THREADS = 256;
+    static constexpr int R = ROWS / 16;  // rows per thread
     static constexpr int CTAS_PER_SM = 2;
     static constexpr int LD = D + 4;  // padded row of Q and K
     static constexpr int LP = KEYS + 4;
@@ -40,9 +43,11 @@ struct SimtCfg {
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
-template <int D>
+template <int D, int ROWS>
 __global__ void __launch_bounds__(256, 2) attn_simt_kernel(const AttnParams p) {
-    using C = SimtCfg<D>;
+    using C = SimtCfg<D, ROWS>;
+    using Div = SimtDivision<ROWS>;
+    constexpr int R = C::R;
     extern __shared__ __align__(16) float simt_smem[];
     float* sq = simt_smem + C::Q_OFF;
     float* sk = simt_smem + C::K_OFF;
@@ -58,7 +63,7 @@ __global__ void __launch_bounds__(256, 2) attn_simt_kernel(const AttnParams p) {
     constexpr int C4 = D / 4;
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    AttnWalk<SimtDivision> walk = attn_walk_start<SimtDivision, C::THREADS>(p, walk_scratch);
+    AttnWalk<Div> walk = attn_walk_start<Div, C::THREADS>(p, walk_scratch);
     for (int n = 0;; ++n) {
         // the walk, by thread 0; a slot is written again only after the barrier of the item between
         if (tid == 0 && !walk.next(p, item[n & 1])) item[n & 1].seq = -1;
@@ -79,9 +84,9 @@ __global__ void __launch_bounds__(256, 2) attn_simt_kernel(const AttnParams p) {
                           (g * G + (r & (G - 1))) * D + 4 * c);
             *reinterpret_cast<float4*>(sq + r * C::LD + c * 4) = v;
         }
-        float m[4], l[4], o[4][4 * OJ];
+        float m[R], l[R], o[R][4 * OJ];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < R; ++i) {
             m[i] = -INFINITY;
             l[i] = 0.f;
 #pragma unroll
@@ -92,39 +97,53 @@ __global__ void __launch_bounds__(256, 2) attn_simt_kernel(const AttnParams p) {
             // K and V rows of the step; rows past the part's end, and of blocks outside the
             // pool, are zeros that no row sees (and that nothing is multiplied into)
             int bad = 0;
-            for (int i = tid; i < C::KEYS * C4; i += C::THREADS) {
-                const int r = i / C4, c = i % C4;
-                const int key = k0 + r;
-                float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
-                if (key < u.kv1) {
-                    const int e = bt[key / bs];
-                    if (e < 0 || e >= p.num_blocks) {
-                        bad = 1;
-                    } else {
-                        const long long at = (((long long)e * Hkv + g) * bs + key % bs) * D;
-                        kv = load4(static_cast<const float*>(p.k_cache) + at + 4 * c);
-                        vv = load4(static_cast<const float*>(p.v_cache) + at + 4 * c);
+            constexpr int N = C::KEYS * C4 / C::THREADS;  // float4 of K, and of V, per thread
+            int e[N];
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const int key = k0 + (tid + n * C::THREADS) / C4;
+                e[n] = key < u.kv1 ? bt[key / bs] : -1;
+                if (key < u.kv1 && (e[n] < 0 || e[n] >= p.num_blocks)) {
+                    bad = 1;
+                    e[n] = -1;
+                }
+            }
+#pragma unroll
+            for (int n0 = 0; n0 < N; n0 += 4) {
+                float4 kv[4], vv[4];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const int i = tid + (n0 + n) * C::THREADS, r = i / C4, c = i % C4;
+                    kv[n] = vv[n] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (e[n0 + n] >= 0 && PKV_DCHECK(p.err, e[n0 + n] < p.num_blocks && g < Hkv)) {
+                        const long long at = (((long long)e[n0 + n] * Hkv + g) * bs + (k0 + r) % bs) * D + 4 * c;
+                        kv[n] = load4(static_cast<const float*>(p.k_cache) + at);
+                        vv[n] = load4(static_cast<const float*>(p.v_cache) + at);
                     }
                 }
-                *reinterpret_cast<float4*>(sk + r * C::LD + c * 4) = kv;
-                *reinterpret_cast<float4*>(sv + r * D + c * 4) = vv;
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const int i = tid + (n0 + n) * C::THREADS, r = i / C4, c = i % C4;
+                    *reinterpret_cast<float4*>(sk + r * C::LD + c * 4) = kv[n];
+                    *reinterpret_cast<float4*>(sv + r * D + c * 4) = vv[n];
+                }
             }
             if (bad) set_error(p.err, PKV_ERR_DEVICE_BOUNDS);
             bad = __syncthreads_or(bad);
-            float s[4][4];
+            float s[R][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < R; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
 #pragma unroll 4
             for (int c = 0; c < C4; ++c) {
-                float4 a[4], b[4];
+                float4 a[R], b[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(sq + (4 * ty + i) * C::LD + 4 * c);
+                for (int i = 0; i < R; ++i) a[i] = *reinterpret_cast<const float4*>(sq + (R * ty + i) * C::LD + 4 * c);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(sk + (tx + 16 * j) * C::LD + 4 * c);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < R; ++i)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
@@ -136,10 +155,10 @@ __global__ void __launch_bounds__(256, 2) attn_simt_kernel(const AttnParams p) {
             // keys every row of the tile sees need no test
             const int seen_by_all = p.parents ? u.first : u.pos + 1;
             const bool masked = bad || k0 + C::KEYS > (seen_by_all < u.kv1 ? seen_by_all : u.kv1);
-            float alpha[4];
+            float alpha[R];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = 4 * ty + i;
+            for (int i = 0; i < R; ++i) {
+                const int r = R * ty + i;
                 float mx = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -172,26 +191,26 @@ __global__ void __launch_bounds__(256, 2) attn_simt_kernel(const AttnParams p) {
             }
             __syncthreads();  // every thread is done with K
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < R; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) sp[(4 * ty + i) * C::LP + tx + 16 * j] = s[i][j];
+                for (int j = 0; j < 4; ++j) sp[(R * ty + i) * C::LP + tx + 16 * j] = s[i][j];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < R; ++i)
 #pragma unroll
                 for (int j = 0; j < 4 * OJ; ++j) o[i][j] *= alpha[i];
             __syncwarp();  // a row's 16 threads are one half of a warp
 #pragma unroll 2
             for (int c = 0; c < C::KEYS / 4; ++c) {
-                float4 a[4];
+                float4 a[R];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(sp + (4 * ty + i) * C::LP + 4 * c);
+                for (int i = 0; i < R; ++i) a[i] = *reinterpret_cast<const float4*>(sp + (R * ty + i) * C::LP + 4 * c);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
 #pragma unroll
                     for (int j = 0; j < OJ; ++j) {
                         const float4 b = *reinterpret_cast<const float4*>(sv + (4 * c + k) * D + 64 * j + 4 * tx);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int i = 0; i < R; ++i) {
                             const float w = k == 0 ? a[i].x : k == 1 ? a[i].y : k == 2 ? a[i].z : a[i].w;
                             if (masked && w == 0.f) continue;  // 0 * inf: an unseen key's V stays out
                             o[i][4 * j + 0] = fmaf(w, b.x, o[i][4 * j + 0]);
@@ -204,13 +223,13 @@ __global__ void __launch_bounds__(256, 2) attn_simt_kernel(const AttnParams p) {
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < R; ++i)
 #pragma unroll
             for (int d = 8; d; d >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = 4 * ty + i;
-            if (r >= rows) continue;
+        for (int i = 0; i < R; ++i) {
+            const int r = R * ty + i;
+            if (r >= rows || !PKV_DCHECK(p.err, u.row + (r >> p.group_log2) < p.num_tokens && r < p.part_rows)) continue;
             if (u.nparts == 1) {
                 const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];  // no key seen: a zero row
                 float* dst = static_cast<float*>(p.out) +
@@ -229,7 +248,7 @@ __global__ void __launch_bounds__(256, 2) attn_simt_kernel(const AttnParams p) {
             }
         }
         if (u.nparts > 1)
-            attn_merge<SimtDivision, float, D, C::THREADS>(p, u, walk.share, &flag, &turns, tid, [] {
+            attn_merge<Div, float, D, C::THREADS>(p, u, walk.share, &flag, &turns, tid, [] {
                 __syncthreads();
                 return true;
             });

@@ -77,12 +77,22 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
                  "r"(bytes)
                  : "memory");
 }
-__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+// Whether the phase is complete: at a look, or after a sleep of at most `ns`.
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
         : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity, uint32_t ns) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(ns)
         : "memory");
     return ok != 0;
 }
@@ -92,7 +102,7 @@ __device__ __forceinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, vol
                                            unsigned long long wait_ns, int* err) {
     const unsigned long long t0 = globaltimer_ns();
     for (;;) {
-        if (__all_sync(0xffffffffu, bar_try(bar, parity))) return true;
+        if (__all_sync(0xffffffffu, bar_try(bar, parity, 1000u))) return true;
         const bool late = globaltimer_ns() - t0 > wait_ns;
         if (__any_sync(0xffffffffu, late || *abort_flag)) {
             if ((threadIdx.x & 31) == 0) {
@@ -324,8 +334,9 @@ struct Cfg {
     static_assert(MMA_DONE + 8 == BAR_OFF + NBARS * 8, "");
     static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;  // tmem address, abort, flag, turns
     static constexpr int ITEM_OFF = (MISC_OFF + 48 + 15) / 16 * 16;
-    static constexpr int WALK_OFF = ITEM_OFF + ITEMS * 64;
-    static constexpr int ML_OFF = WALK_OFF + (THREADS / 32 + 8) * 8;  // float2[128]
+    static constexpr int WALK_OFF = ITEM_OFF + ITEMS * 64;  // the CTA's walk, as it starts
+    static constexpr int ML_OFF = WALK_OFF + 64;            // float2[128]; first the scratch of the walk's start
+    static_assert((THREADS / 32 + 8) * 8 <= 128 * 8 && sizeof(AttnWalk<TcDivision>) <= 64, "");
     static constexpr int SMEM_BYTES = ML_OFF + 128 * 8 + 1024;
     static_assert(SMEM_BYTES <= 232448, "227 KB of shared memory");
     static_assert(sizeof(AttnItem) <= 64, "");
@@ -501,7 +512,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const AttnWalk<TcDivision> walk0 =
-        attn_walk_start<TcDivision, C::THREADS>(p, reinterpret_cast<long long*>(smem + C::WALK_OFF));
+        attn_walk_start<TcDivision, C::THREADS>(p, reinterpret_cast<long long*>(smem + C::ML_OFF));
+    if (tid == 0) *reinterpret_cast<AttnWalk<TcDivision>*>(smem + C::WALK_OFF) = walk0;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -512,7 +524,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
 
     // A wait by a converged warp; false: wind down.
     auto wait = [&](uint32_t off, uint32_t parity) -> bool {
-        if (__all_sync(0xffffffffu, bar_try(sb + off, parity))) return true;
+        if (__all_sync(0xffffffffu, bar_test(sb + off, parity))) return true;
         return bar_wait_slow(sb + off, parity, abort_flag, p.wait_ns, p.err);
     };
     auto arrive = [&](uint32_t off) {  // once for the warp, after what its lanes did
@@ -521,9 +533,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     };
     // Items in the order in which the walk puts them into the ring; false: no more, or wind down.
     static_assert((C::ITEMS & (C::ITEMS - 1)) == 0, "");
-    auto take_item = [&](int n, AttnItem& u) -> bool {
+    auto take_item = [&](int n, AttnItem& u, bool& ok) -> bool {
         const uint32_t i = n & (C::ITEMS - 1);
-        if (!wait(C::ITEM_FULL + 8 * i, (n / C::ITEMS) & 1)) return false;
+        if (!(ok = wait(C::ITEM_FULL + 8 * i, (n / C::ITEMS) & 1))) return false;
         u = *reinterpret_cast<const AttnItem*>(smem + C::ITEM_OFF + i * 64);
         arrive(C::ITEM_EMPTY + 8 * i);
         return u.seq >= 0;
@@ -552,7 +564,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             // ------------------------------------------------------- producer
             uint32_t st = 0, phase = 1;  // slot, parity of its emptying (the first round finds them empty)
             AttnItem u;
-            for (int n = 0; take_item(n, u); ++n) {
+            bool ok = true;
+            for (int n = 0; ok && take_item(n, u, ok); ++n) {
                 Plan plan;
                 plan.set(u, gl);
                 if (plan.steps == 0) continue;
@@ -569,7 +582,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     return -1;
                 };
                 int e = entry(0), e1 = entry(1);
-                bool ok = true;
                 for (int l = 0; l < n_loads; ++l) {
                     const int e2 = entry(l + 2);  // two loads ahead of its use
                     if (!(ok = wait(C::LOAD_EMPTY + 8 * st, phase))) break;
@@ -584,7 +596,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                             bar_arrive(full);
                     }
                     __syncwarp();  // the expected byte count is registered before any copy lands
-                    if (e >= 0) {
+                    if (e >= 0 && PKV_DCHECK(p.err, e < p.num_blocks && u.g < Hkv && lane < bpt)) {
                         const CUtensorMap* map = v ? &tmv : &tmk;
                         uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::LOAD_FULL + 8 * st);
                         if constexpr (FP8)
@@ -660,7 +672,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                            C::IDESC_PV, kk > 0 ? 1u : accumulate, one);
             };
             AttnItem u;
-            for (int n = 0; ok && take_item(n, u); ++n) {
+            for (int n = 0; ok && take_item(n, u, ok); ++n) {
                 Plan plan;
                 plan.set(u, gl);
                 if (plan.steps == 0) continue;
@@ -761,7 +773,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             return r;
         };
         AttnItem u;
-        for (int n = 0; ok && take_item(n, u); ++n) {
+        for (int n = 0; ok && take_item(n, u, ok); ++n) {
             Plan plan;
             plan.set(u, gl);
             const int rows = u.ntok << gl;
@@ -964,7 +976,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 }
                 tc_fence_after();
                 const int rows_left = rows - row0;  // of this warp
-                const bool here = row < rows;
+                const bool here = row < rows && PKV_DCHECK(p.err, u.row + (row >> gl) < p.num_tokens && row < p.part_rows);
                 const bool split = u.nparts > 1, few = u.nparts <= FEW_PARTS;
                 const int slot = attn_partial(blockIdx.x, u.part);
                 int* count = split ? p.counters + AttnWalk<TcDivision>::owner(u, walk0.share, 0) * 8 + (warp & 7)
@@ -1168,6 +1180,24 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     break;
             }
         }
+        if (!ok && lane == 0) {
+            // given up: parts that this warp has not counted become empty ones, so that the
+            // counters end at zero and the others' results meet nothing stale
+            AttnWalk<TcDivision> walk = *reinterpret_cast<const AttnWalk<TcDivision>*>(smem + C::WALK_OFF);
+            int k = 0;
+            while (walk.next(p, u)) {
+                const int n_rows = u.ntok << gl, first_row = n_rows > 128 ? warp * 32 : (warp & 3) * 32;
+                const bool few = u.nparts <= FEW_PARTS;
+                if (u.nparts == 1 || (few ? first_row >= n_rows || (n_rows <= 128 && warp >= 4) : warp > 0)) continue;
+                if (k++ < turns[warp]) continue;
+                const int n = few && n_rows > first_row + 32 ? first_row + 32 : n_rows;
+                for (int r = few ? first_row : 0; r < n; ++r)
+                    p.ws_ml[(long long)attn_partial(blockIdx.x, u.part) * p.part_rows + r] = make_float2(-INFINITY, 0.f);
+                __threadfence();
+                int* c = p.counters + AttnWalk<TcDivision>::owner(u, walk.share, 0) * 8 + warp;
+                if (atomicAdd(c, 1) == u.nparts - 1) *c = 0;
+            }
+        }
     } else {
         // ----------------------------------------------------------- widening
         if constexpr (FP8) {
@@ -1176,7 +1206,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             uint32_t rs = 0, raw_phase = 0, st = 0, empty_phase = 1;
             bool ok = true;
             AttnItem u;
-            for (int n = 0; ok && take_item(n, u); ++n) {
+            for (int n = 0; ok && take_item(n, u, ok); ++n) {
                 Plan plan;
                 plan.set(u, gl);
                 if (plan.steps == 0) continue;
@@ -1243,7 +1273,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
         // copies and products in flight land before the CTA leaves; each wait is bounded
         auto land = [&](uint32_t off, uint32_t parity) {
             const unsigned long long t0 = globaltimer_ns();
-            while (!bar_try(sb + off, parity))
+            while (!bar_try(sb + off, parity, 1000u))
                 if (globaltimer_ns() - t0 > kWaitTimeoutNs) break;
         };
         if (warp == 8 && lane == 0) {
@@ -1254,25 +1284,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
         if (warp == 9 && mma_any) {
             commit_one(sb + C::MMA_DONE, elect_one());
             land(C::MMA_DONE, 0);
-        }
-        // parts that were not counted: empty ones, so that the counters end at zero
-        AttnWalk<TcDivision> walk =
-            attn_walk_start<TcDivision, C::THREADS>(p, reinterpret_cast<long long*>(smem + C::WALK_OFF));
-        if (warp < 8 && lane == 0) {
-            AttnItem u;
-            int k = 0;
-            while (walk.next(p, u)) {
-                const int n_rows = u.ntok << gl, first_row = n_rows > 128 ? warp * 32 : (warp & 3) * 32;
-                const bool few = u.nparts <= FEW_PARTS;
-                if (u.nparts == 1 || (few ? first_row >= n_rows || (n_rows <= 128 && warp >= 4) : warp > 0)) continue;
-                if (k++ < turns[warp]) continue;
-                const int n = few && n_rows > first_row + 32 ? first_row + 32 : n_rows;
-                for (int r = few ? first_row : 0; r < n; ++r)
-                    p.ws_ml[(long long)attn_partial(blockIdx.x, u.part) * p.part_rows + r] = make_float2(-INFINITY, 0.f);
-                __threadfence();
-                int* c = p.counters + AttnWalk<TcDivision>::owner(u, walk.share, 0) * 8 + warp;
-                if (atomicAdd(c, 1) == u.nparts - 1) *c = 0;
-            }
         }
         tc_fence_before();
         __syncthreads();

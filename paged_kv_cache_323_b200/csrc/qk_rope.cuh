@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) qk_rope_kernel(const RopePara
     // a row of a pool
     auto store = [&](void* cache, const float* scales, int j, int g, const float2* x) {
         const long long row = rows_at[j];
-        if (row < 0) return;
+        if (row < 0 || !PKV_DCHECK(p.err, row + (long long)g * p.block_size < p.num_slots * Hkv && j < tokens)) return;
         const long long at = (row + (long long)g * p.block_size) * D;
         if constexpr (FP8) {
             uint8_t* to = static_cast<uint8_t*>(cache) + at;
