@@ -102,7 +102,7 @@ __device__ __forceinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, vol
                                            unsigned long long wait_ns, int* err) {
     const unsigned long long t0 = globaltimer_ns();
     for (;;) {
-        if (__all_sync(0xffffffffu, bar_try(bar, parity, 1000u))) return true;
+        if (__all_sync(0xffffffffu, bar_try(bar, parity, 500u))) return true;
         const bool late = globaltimer_ns() - t0 > wait_ns;
         if (__any_sync(0xffffffffu, late || *abort_flag)) {
             if ((threadIdx.x & 31) == 0) {
@@ -524,9 +524,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
 
     // A wait by a converged warp; false: wind down.
     auto wait = [&](uint32_t off, uint32_t parity) -> bool {
-        // with the widening warps about, a first look that sleeps is 4 % faster (1.16 against
-        // 1.21 ms over 15K-token fp8 contexts), without them 1 % slower
-        if (__all_sync(0xffffffffu, FP8 ? bar_try(sb + off, parity, 1000u) : bar_test(sb + off, parity))) return true;
+        if (__all_sync(0xffffffffu, bar_test(sb + off, parity))) return true;
         return bar_wait_slow(sb + off, parity, abort_flag, p.wait_ns, p.err);
     };
     auto arrive = [&](uint32_t off) {  // once for the warp, after what its lanes did
