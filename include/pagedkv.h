@@ -11,7 +11,9 @@
  * and V through the table (item 5), the append of new tokens' K/V into their
  * slots (section "The problem: the KV cache is big and unpredictable": the
  * cache grows by one entry per new token), and the block copy of
- * copy-on-write (section "Sharing blocks between sequences").
+ * copy-on-write (section "Sharing blocks between sequences").  Around them, over
+ * the same pools: the q/k norm and rotation with the append, and the attention
+ * of whole prompts and of drafted token trees.
  *
  * Conventions shared by every call
  * --------------------------------
