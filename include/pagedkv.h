@@ -290,8 +290,8 @@ PKV_API int qk_norm_rope_append_fp8(void* q_out, const void* q, const void* k, c
  * qk_norm_rope_append of the same step).  The i-th of them attends keys
  * 0 .. context_lens[s] - n + i.
  *   query_start  int32 [num_seqs + 1], not decreasing, from 0.  Rows from
- *                query_start[num_seqs] to num_tokens, which pad the batch, are
- *                neither read nor written.
+ *                query_start[num_seqs] to num_tokens, which pad the batch, may hold
+ *                anything and stay as they are in out.
  *   q            [num_tokens][num_heads][head_dim], q_stride elements between
  *                two tokens (a multiple of 16 bytes); out is contiguous.
  *   workspace    at least paged_attention_prefill_workspace_size bytes,

@@ -2,7 +2,7 @@
 // argument validation, status codes, launch selection, the library-owned
 // split-K workspace, the per-device error word and the launch profiler.
 // Every compute step runs in the kernels of decode_attn.cuh, decode_tc.cuh,
-// decode_tc_fp8.cuh and kv_ops.cuh.
+// decode_tc_fp8.cuh, kv_ops.cuh, attn_tc.cuh, attn_simt.cuh and qk_rope.cuh.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>

@@ -79,6 +79,28 @@ def test_strided_q(pk, dtype, tree):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "fp8"])
+def test_out_at_any_16_bytes(pk, dtype):
+    """out, q and the pools at addresses that are multiples of 16 bytes and no more."""
+    b = Batch([(70, 300), (130, 130), (5, 5000)], dtype=dtype, heads=8, kv_heads=2, seed=7)
+    b.poison()
+    ref, bound = attend(b)
+
+    def moved(t):
+        n = 16 // t.element_size()
+        raw = torch.empty(t.numel() + 64, dtype=t.dtype, device="cuda")
+        at = next(i for i in range(n, 64, n) if (raw.data_ptr() + i * t.element_size()) % 32)
+        to = raw[at:at + t.numel()].view(t.shape)
+        to.view(torch.uint8).copy_(t.contiguous().view(torch.uint8))
+        return to
+
+    b.out, b.q, b.kc, b.vc = moved(b.out), moved(b.q), moved(b.kc), moved(b.vc)
+    got = b.call(pk)
+    torch.cuda.synchronize()
+    assert pk.get_device_error() == 0
+    close(got, ref, bound)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "fp8"])
 @pytest.mark.parametrize("scale", [0.0, -0.3, 4.0])
 def test_scales(pk, dtype, scale):
     b = Batch([(40, 300), (130, 130)], dtype=dtype, heads=8, kv_heads=2, seed=5)
@@ -218,6 +240,28 @@ def test_chain_is_prefill_and_one_token_is_decode(pk, dtype):
     for s, (n, _) in enumerate(b.seqs):
         b.parents[b.start_host[s]:b.start_host[s] + n] = torch.arange(-1, n - 1, device="cuda", dtype=torch.int32)
     assert torch.equal(b.call(pk, True).clone(), b.call(pk, False))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "fp8"])
+def test_blocks_shared_between_sequences(pk, dtype):
+    """Sequences whose tables name the same prefix blocks, one of them twice."""
+    b = Batch([(33, 400), (40, 420), (7, 300)], dtype=dtype, heads=4, kv_heads=2, seed=23)
+    b.tables[1, :20] = b.tables[0, :20]
+    b.tables[2, :10] = b.tables[0, 0]
+    ref, bound = attend(b, True)
+    close(b.call(pk, True), ref, bound)
+    assert pk.get_device_error() == 0
+
+
+def test_every_row_of_nan(pk):
+    """A cache of NaN: every row, whole and split items, comes out NaN."""
+    b = Batch([(40, 90), (5, 3000)], dtype="bf16", heads=2, kv_heads=1, seed=24)
+    b.vc[:] = math.nan
+    assert bool(torch.isnan(b.call(pk)).all())
+    b = Batch([(40, 90), (5, 3000)], dtype="bf16", heads=2, kv_heads=1, seed=24)
+    b.kc[:] = math.nan
+    assert bool(torch.isnan(b.call(pk)).all())
+    assert pk.get_device_error() == 0
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "fp8"])
