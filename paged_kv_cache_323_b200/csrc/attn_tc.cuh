@@ -628,7 +628,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             // ------------------------------------------------------ MMA issue
             // The tensor cores hold a few instructions in advance, some 250 clocks of work.
             // What this warp does between two of them has to fit into that, so waits and
-            // bookkeeping are spread: after six of a product's eight, between two products
+            // bookkeeping are spread: after four of a product's eight, between two products
             // and in the middle of QK^T.
             const uint32_t one = elect_one();
             // descriptors of the first tile; others differ in the address field (16-byte units)
@@ -660,14 +660,14 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 }
                 if (half == 1) commit_one(sb + C::S_FULL + 8 * i, one);
             };
-            // keys 0 .. 95 and 96 .. 127 of O_i += P V
+            // keys 0 .. 63 and 64 .. 127 of O_i += P V
             auto pv = [&](int i, uint32_t st, uint32_t phase, uint32_t accumulate, int part) {
                 const uint32_t b = v_lo + st * (C::TILE >> 4);
                 ok = ok && wait((part == 0 ? C::P_FULL : C::P_REST) + 8 * i, phase);
                 if (!ok) return;
                 tc_fence_after();
 #pragma unroll
-                for (int kk = part == 0 ? 0 : 6; kk < (part == 0 ? 6 : 8); ++kk)
+                for (int kk = 4 * part; kk < 4 * part + 4; ++kk)
                     mma_ts(tmem + C::O_COL + i * 128, tmem + i * 128 + kk * 8, b + ((kk * 2 * C::GSTRIDE) >> 4), v_hi,
                            C::IDESC_PV, kk > 0 ? 1u : accumulate, one);
             };
@@ -881,7 +881,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                             for (int e = 0; e < 16; ++e) pk[e] = 0u;
                         }
                         tmem_st16(t_s + 16 * c, pk);  // over scores that have been read
-                        if (c == 2) {
+                        if (c == 1) {
                             tmem_wait_st();
                             if (!(ok = o_readable())) break;
                             tc_fence_before();
@@ -889,39 +889,30 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                         }
                     }
                 } else {
-                    // (with the registers of the fp8 kernel, 64 keys at a time)
-                    constexpr int AT_ONCE = FP8 ? 64 : 128;
-                    float x[AT_ONCE];
-                    uint32_t pk[AT_ONCE == 128 ? 48 : 32];
-#pragma unroll
-                    for (int c = 0; c < AT_ONCE / 32; ++c) tmem_ld32(t_s + 32 * c, x + 32 * c);
-                    tmem_wait_ld();
-                    if (t == 0) {
-                        m = largest32(x, -INFINITY) * qa;  // the row's reference
-                        if (!(ok = o_readable())) break;
-                    }
-                    const float2 m2 = make_float2(-m, -m);
-                    if constexpr (AT_ONCE == 128) {
-#pragma unroll
-                        for (int c = 0; c < 3; ++c) weights<32>(x + 32 * c, q2, m2, pk + 16 * c, sum);
-                        tmem_st32(t_s, pk);
-                        tmem_st16(t_s + 32, pk + 32);
-                    } else {
+                    // 64 keys at a time, in a loop: shorter code than the 128 in a row, which kept
+                    // the roles waiting for instructions (4096 tokens of 16 heads: 102 us in a row,
+                    // 97 in a loop)
+#pragma unroll 1
+                    for (int c = 0; c < 2; ++c) {
+                        float x[64];
+                        uint32_t pk[32];
+                        tmem_ld32(t_s + 64 * c, x);
+                        tmem_ld32(t_s + 64 * c + 32, x + 32);
+                        tmem_wait_ld();
+                        if (t == 0 && c == 0) {
+                            m = largest32(x, -INFINITY) * qa;  // the row's reference
+                            if (!(ok = o_readable())) break;
+                        }
+                        const float2 m2 = make_float2(-m, -m);
                         weights<32>(x, q2, m2, pk, sum);
                         weights<32>(x + 32, q2, m2, pk + 16, sum);
-                        tmem_ld32(t_s + 64, x);
-                        tmem_ld32(t_s + 96, x + 32);
-                        tmem_st32(t_s, pk);
-                        tmem_wait_ld();
-                        weights<32>(x, q2, m2, pk, sum);
-                        tmem_st16(t_s + 32, pk);
+                        tmem_st32(t_s + 32 * c, pk);
+                        if (c == 0) {
+                            tmem_wait_st();
+                            tc_fence_before();
+                            arrive(C::P_FULL + 8 * wg);
+                        }
                     }
-                    tmem_wait_st();
-                    // the product of the first 96 keys may start
-                    tc_fence_before();
-                    arrive(C::P_FULL + 8 * wg);
-                    weights<32>(x + AT_ONCE - 32, q2, m2, pk, sum);
-                    tmem_st16(t_s + 48, pk);
                 }
                 if (!ok) break;
                 tmem_wait_st();
@@ -1225,7 +1216,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     const unsigned char* raw = smem + C::RAW_OFF + rs * C::RAW;
                     unsigned char* wide = smem + C::SLOT_OFF + st * C::TILE;
                     constexpr int CPR = D / 16;  // 16-byte chunks of a raw row
-#pragma unroll
+                    // (unrolled, this loop takes the whole kernel longer: 1205 us against 1087 on
+                    // 1024-token chunks over 15K contexts, for the same reason)
+#pragma unroll 1
                     for (int i = 0; i < C::KEYS * CPR / C::WIDEN; ++i) {
                         const int x = tw + C::WIDEN * i, r = x / CPR, c = x % CPR;
                         uint4 w = *reinterpret_cast<const uint4*>(raw + x * 16);
