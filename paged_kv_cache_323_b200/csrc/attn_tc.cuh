@@ -251,9 +251,11 @@ __device__ __forceinline__ void store_sector(void* to, const uint32_t (&r)[8]) {
 
 // Weights 2^(x q + m) of N scores of a row, packed for the MMA; sum gets their
 // total.  One pair in POLY_OF goes by ex2_poly, so that the special-function
-// unit (a quarter of the lanes a clock) and the FMA pipe share the work.
+// unit (a quarter of the lanes a clock) and the FMA pipe share the work; not
+// over fp8 caches (952 us with it, 931 without, on 1024-token chunks over 15K
+// contexts), where widening is what keeps the pipes busy.
 constexpr int POLY_OF = 8;
-template <int N, bool POLY = true>
+template <int N, bool POLY>
 __device__ __forceinline__ void weights(const float* x, float2 q, float2 m, uint32_t* pk, float2& sum) {
     float2 sum1 = make_float2(0.f, 0.f);
 #pragma unroll
@@ -639,7 +641,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                            k_hi = (uint32_t)(k_desc >> 32), v_lo = (uint32_t)v_desc, v_hi = (uint32_t)(v_desc >> 32);
             uint32_t idesc_qk = 0;
             uint32_t slot = 0, slot_phase = 0;  // loads are used in their order
-            uint32_t q_phase = 0, p_phase0 = 0, p_phase1 = 0;
+            uint32_t q_phase = 0, p_phases = 0;  // a bit for each pipeline
             bool ok = true;
             auto next_load = [&]() -> uint32_t {
                 const uint32_t st = slot;
@@ -687,60 +689,52 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 uint32_t ks = next_load(), vs = 0;
                 if (!ok) break;
                 tc_fence_after();
-                if (n0 > 0) {
-                    qk(0, 0, ks, 0);
-                    qk(0, 0, ks, 1);
+#pragma unroll (FP8 ? 1 : 2)
+                for (int i = 0; i < 2; ++i) {
+                    if (i == 1 && !wide) {  // its own K tile
+                        release(ks);
+                        --left;
+                        if (n1 > 0) ks = next_load();
+                    }
+                    if (!ok || (i ? n1 : n0) == 0) continue;
+                    qk(i, wide ? i : 0, ks, 0);
+                    qk(i, wide ? i : 0, ks, 1);
+                    if (i == 1) {
+                        release(ks);
+                        --left;
+                    }
                 }
-                if (!wide) {
-                    release(ks);
-                    --left;
-                    if (n1 > 0) ks = next_load();
-                    if (!ok) break;
-                }
-                if (n1 > 0) {
-                    qk(1, wide, ks, 0);
-                    qk(1, wide, ks, 1);
-                    release(ks);
-                    --left;
-                }
+                if (!ok) break;
                 if (left == 0) commit_one(sb + C::Q_EMPTY, one);
                 vs = next_load();
                 const int nmax = n0 > n1 ? n0 : n1;
-                for (int t = 0; t < nmax; ++t) {
-                    if (t < n0) {
-                        const bool more = t + 1 < n0;
-                        pv(0, vs, p_phase0, t > 0, 0);
-                        if (more) ks = next_load();
-                        pv(0, vs, p_phase0, t > 0, 1);
-                        if (!ok) break;
-                        p_phase0 ^= 1;
-                        if (more) qk(0, 0, ks, 0);
-                        else commit_one(sb + C::O_FULL, one);
-                        if (!wide) {
-                            release(vs);
-                            if (t < n1) vs = next_load();
-                        }
-                        if (more) {
-                            qk(0, 0, ks, 1);
-                            if (!wide) {
-                                release(ks);
-                                if (--left == 0) commit_one(sb + C::Q_EMPTY, one);
-                            }
-                        }
-                    }
-                    if (t < n1) {
-                        const bool more = t + 1 < n1;
-                        pv(1, vs, p_phase1, t > 0, 0);
-                        if (more && (!wide || t + 1 >= n0)) ks = next_load();
-                        pv(1, vs, p_phase1, t > 0, 1);
-                        if (!ok) break;
-                        p_phase1 ^= 1;
-                        if (more) qk(1, wide, ks, 0);
-                        else commit_one(sb + C::O_FULL + 8, one);
+                // Steps of the pipelines by turns.  Code that serves both is shorter, code for each
+                // has its addresses ready: fp8 kernels, with one role more to hold in the
+                // instruction caches, gain by the first (156 -> 147 us on the drafted trees of 24
+                // sequences), bf16 kernels by the second (82 against 84 us on packed prompts).
+#pragma unroll (FP8 ? 1 : 2)
+                for (int x = 0; x < 2 * nmax; ++x) {
+                    const int i = x & 1, t = x >> 1, mine = i ? n1 : n0, other = i ? n0 : n1;
+                    if (t >= mine) continue;
+                    const bool more = t + 1 < mine;
+                    const bool lone = !wide || i == 1;             // this pipeline is the last to want its tiles
+                    const uint32_t phase = p_phases >> i & 1;
+                    pv(i, vs, phase, t > 0, 0);
+                    // wide: pipeline 0 brings the next K for both, while it goes on
+                    if (more && (!wide || i == 0 || t + 1 >= n0)) ks = next_load();
+                    pv(i, vs, phase, t > 0, 1);
+                    if (!ok) break;
+                    p_phases ^= 1u << i;
+                    if (more) qk(i, wide ? i : 0, ks, 0);
+                    else commit_one(sb + C::O_FULL + 8 * i, one);
+                    if (lone) {
                         release(vs);
-                        if (more || t + 1 < n0) vs = next_load();
-                        if (more) {
-                            qk(1, wide, ks, 1);
+                        // the V of what comes next: the other pipeline's step, or this one's
+                        if (i == 0 ? t < other : more || t + 1 < other) vs = next_load();
+                    }
+                    if (more) {
+                        qk(i, wide ? i : 0, ks, 1);
+                        if (lone) {
                             release(ks);
                             if (--left == 0) commit_one(sb + C::Q_EMPTY, one);
                         }
@@ -904,8 +898,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                             if (!(ok = o_readable())) break;
                         }
                         const float2 m2 = make_float2(-m, -m);
-                        weights<32>(x, q2, m2, pk, sum);
-                        weights<32>(x + 32, q2, m2, pk + 16, sum);
+                        weights<32, !FP8>(x, q2, m2, pk, sum);
+                        weights<32, !FP8>(x + 32, q2, m2, pk + 16, sum);
                         tmem_st32(t_s + 32 * c, pk);
                         if (c == 0) {
                             tmem_wait_st();
@@ -1193,7 +1187,15 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
         // ----------------------------------------------------------- widening
         if constexpr (FP8) {
             regs_dec<C::REGS_WIDEN>();
-            const int tw = tid - 384;
+            // A thread's 16-byte chunks of a raw tile: the same place c of rows r0, r0 + RSTEP, ..;
+            // widened they are two chunks.  Threads with the second half of a row store them in the
+            // other order: no bank conflicts.
+            constexpr int CPR = D / 16, RSTEP = C::WIDEN / CPR;
+            static_assert(RSTEP % 8 == 0, "rows of a thread have the same place in the swizzle");
+            const int tw = tid - 384, c = tw % CPR, r0 = tw / CPR, second = (c >> 2) & 1;
+            const int to0 = (r0 >> 3) * C::GSTRIDE + (c >> 2) * C::HSTEP + (r0 & 7) * 128;
+            const int to_a = to0 + (((2 * (c & 3) + second) ^ (r0 & 7)) << 4);
+            const int to_b = to0 + (((2 * (c & 3) + 1 - second) ^ (r0 & 7)) << 4);
             uint32_t rs = 0, raw_phase = 0, st = 0, empty_phase = 1;
             bool ok = true;
             AttnItem u;
@@ -1210,18 +1212,16 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     const uint32_t bad = __ballot_sync(0xffffffffu, e < 0 || e >= p.num_blocks);
                     const bool short_step = k0 + C::KEYS > u.kv1 || bad != 0;
                     uint32_t there[4];
-                    there_words(u.kv1 - k0, bad, bs, there);
+                    if (short_step) there_words(u.kv1 - k0, bad, bs, there);
                     if (!(ok = wait(C::LOAD_FULL + 8 * rs, raw_phase))) break;
                     if (!(ok = wait(C::SLOT_EMPTY + 8 * st, empty_phase))) break;
-                    const unsigned char* raw = smem + C::RAW_OFF + rs * C::RAW;
+                    const unsigned char* raw = smem + C::RAW_OFF + rs * C::RAW + tw * 16;
                     unsigned char* wide = smem + C::SLOT_OFF + st * C::TILE;
-                    constexpr int CPR = D / 16;  // 16-byte chunks of a raw row
-                    // (unrolled, this loop takes the whole kernel longer: 1205 us against 1087 on
-                    // 1024-token chunks over 15K contexts, for the same reason)
+                    // (in full unrolled, this loop made the whole kernel a tenth slower, by two 3 %: the
+                    // instruction caches hold its code beside the softmax's)
 #pragma unroll 1
-                    for (int i = 0; i < C::KEYS * CPR / C::WIDEN; ++i) {
-                        const int x = tw + C::WIDEN * i, r = x / CPR, c = x % CPR;
-                        uint4 w = *reinterpret_cast<const uint4*>(raw + x * 16);
+                    for (int r = r0; r < C::KEYS; r += RSTEP) {
+                        uint4 w = *reinterpret_cast<const uint4*>(raw);
                         if (short_step) {
                             const uint32_t word = r < 32 ? there[0] : r < 64 ? there[1] : r < 96 ? there[2] : there[3];
                             if (!(word >> (r & 31) & 1)) w = make_uint4(0u, 0u, 0u, 0u);
@@ -1241,12 +1241,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                                 y[2 * e2 + k] = pack_bf16(f.x, f.y);
                             }
                         }
-                        unsigned char* to = wide + (r >> 3) * C::GSTRIDE + (c >> 2) * C::HSTEP + (r & 7) * 128;
-                        // lanes of the second half store their chunks in the other order: no bank conflicts
-                        const int first = (c >> 2) & 1, cc = 2 * (c & 3);
                         const uint4 a = make_uint4(y[0], y[1], y[2], y[3]), b = make_uint4(y[4], y[5], y[6], y[7]);
-                        *reinterpret_cast<uint4*>(to + (((cc + first) ^ (r & 7)) << 4)) = first ? b : a;
-                        *reinterpret_cast<uint4*>(to + (((cc + 1 - first) ^ (r & 7)) << 4)) = first ? a : b;
+                        *reinterpret_cast<uint4*>(wide + to_a) = second ? b : a;
+                        *reinterpret_cast<uint4*>(wide + to_b) = second ? a : b;
+                        raw += C::WIDEN * 16;
+                        wide += RSTEP / 8 * C::GSTRIDE;
                     }
                     fence_proxy_async_smem();
                     arrive(C::SLOT_FULL + 8 * st);
