@@ -23,7 +23,7 @@ LIB = os.path.join(PKG, "libpagedkv.so")
 LIB_DEBUG = os.path.join(PKG, "libpagedkv_debug.so")
 SOURCES = ["api.cu", "decode_f32.cu", "decode_bf16.cu", "decode_fp8.cu", "decode_tc.cu", "decode_tc_fp8.cu",
            "decode_tc_fp8p.cu", "decode_tc_fp8_d64.cu", "decode_reg.cu",
-           "noalloc.cu", "attn_simt.cu", "attn_tc.cu", "qk_rope.cu",
+           "noalloc.cu", "attn_simt.cu", "attn_tc.cu", "attn_division.cu", "qk_rope.cu",
            "block_manager.cpp"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + [

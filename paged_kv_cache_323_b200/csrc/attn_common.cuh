@@ -77,30 +77,32 @@ struct AttnSeq {
     int q0, n, first;  // first row, queries, position of the first query
     bool valid;        // false: no valid context; its rows are written as zeros
 
-    __device__ __forceinline__ void load(const AttnParams& p, int s, bool report) {
+    __host__ __device__ __forceinline__ void load(const AttnParams& p, int s, bool report) {
         q0 = p.query_start[s];
         const int q1 = p.query_start[s + 1], ctx = p.context_lens[s];
         const bool rows_ok = q0 >= 0 && q1 >= q0 && q1 <= p.num_tokens;
         n = rows_ok ? q1 - q0 : 0;
         valid = rows_ok && ctx >= n && ctx <= (long long)p.max_blocks_per_seq * p.block_size;
         first = valid ? ctx - n : 0;
+#ifdef __CUDA_ARCH__
         if (report && !valid) set_error(p.err, PKV_ERR_DEVICE_BOUNDS);
+#endif
     }
-    __device__ __forceinline__ int tiles(int tt) const { return (n + tt - 1) / tt; }
+    __host__ __device__ __forceinline__ int tiles(int tt) const { return (n + tt - 1) / tt; }
     // keys tile t visits: those up to its last query's own position
-    __device__ __forceinline__ int keys(int t, int tt) const {
+    __host__ __device__ __forceinline__ int keys(int t, int tt) const {
         if (!valid) return 0;
         const long long end = (long long)(t + 1) * tt;
         return first + (end < n ? (int)end : n);
     }
     // work per key of tile t
     template <class Div>
-    __device__ __forceinline__ int per_key(int t, int tt, int group_log2) const {
+    __host__ __device__ __forceinline__ int per_key(int t, int tt, int group_log2) const {
         return Div::per_key((n - t * tt < tt ? n - t * tt : tt) << group_log2);
     }
     // work of the tiles before tile t, for one kv head
     template <class Div>
-    __device__ __forceinline__ long long before(int t, int tt, int group_log2) const {
+    __host__ __device__ __forceinline__ long long before(int t, int tt, int group_log2) const {
         const int last = tiles(tt) - 1;
         const int full = t <= last ? t : last;  // tiles that are surely full
         if (full < 0) return 0;
@@ -132,10 +134,11 @@ struct AttnWalk {
     AttnSeq q;
 
     // key at which a boundary `o` past the start of an item of K keys, f each, cuts it
-    __device__ __forceinline__ static int cut(long long o, int K, int f, long long share) {
+    __host__ __device__ __forceinline__ static int cut(long long o, int K, int f, long long share) {
         if (o <= 0) return 0;
         if (o >= (long long)K * f) return K;
-        const int k = (int)o / f;
+        // o passes 31 bits: up to 2^31 keys times f
+        const int k = (int)(f == Div::MORE ? (unsigned long long)o / Div::MORE : (unsigned long long)o / Div::LESS);
         if (share >= Div::COARSE * f) return k & ~(Div::FINE - 1);
         const int most = K > Div::COARSE ? K - Div::COARSE : 0;  // no part shorter than COARSE
         return (k < most ? k : most) & ~(Div::COARSE - 1);
@@ -144,14 +147,14 @@ struct AttnWalk {
     // COARSE keys every boundary but one short of FINE keys makes a cut; with a
     // smaller one every multiple of COARSE up to K - COARSE is cut, and a part
     // belongs to the last CTA that starts before the part's end.
-    __device__ __forceinline__ static int owner(const AttnItem& it, long long share, int i) {
+    __host__ __device__ __forceinline__ static int owner(const AttnItem& it, long long share, int i) {
         const int b0 = (int)(it.at / share), f = it.per_key, K = it.keys;
         const long long o1 = (b0 + 1) * share - it.at;
         if (share >= Div::COARSE * f) return b0 + i + (o1 < Div::FINE * f && o1 < (long long)K * f ? 1 : 0);
         const long long e = i + 1 < parts(it, share) ? (long long)(i + 1) * Div::COARSE * f : (long long)K * f;
         return b0 + (int)((it.at - b0 * share + e - 1) / share);
     }
-    __device__ __forceinline__ static int parts(const AttnItem& it, long long share) {
+    __host__ __device__ __forceinline__ static int parts(const AttnItem& it, long long share) {
         const int f = it.per_key, K = it.keys;
         if (share >= Div::COARSE * f) {
             const long long o1 = (it.at / share + 1) * share - it.at, all = (long long)K * f;
@@ -161,8 +164,8 @@ struct AttnWalk {
         return K < Div::COARSE ? 1 : K / Div::COARSE;
     }
 
-    // The next item with work for this CTA.
-    __device__ bool next(const AttnParams& p, AttnItem& it) {
+    // The next item with work for CTA `cta`.
+    __host__ __device__ bool next(const AttnParams& p, int cta, AttnItem& it) {
         while (at < end) {
             const int K = q.keys(t, tt), f = q.template per_key<Div>(t, tt, p.group_log2);
             const long long c = (long long)K * f + Div::ITEM, a = begin - at;
@@ -186,7 +189,7 @@ struct AttnWalk {
                 if (k0 > 0 || k1 < K) {
                     it.nparts = parts(it, share);
                     // with large shares the parts' owners follow one another
-                    it.part = share >= Div::COARSE * f ? (int)blockIdx.x - owner(it, share, 0) : k0 / Div::COARSE;
+                    it.part = share >= Div::COARSE * f ? cta - owner(it, share, 0) : k0 / Div::COARSE;
                 }
             }
             at += c;
@@ -206,6 +209,23 @@ struct AttnWalk {
         return false;
     }
 };
+
+// The item of a sequence that the work `o` past the sequence's start falls in:
+// tile, kv head and the item's own start.
+template <class Div>
+__host__ __device__ __forceinline__ void attn_place(const AttnSeq& q, int tt, int group_log2, int kv_heads, long long o,
+                                                    int& tile, int& g, long long& at) {
+    int lo = 0, hi = q.tiles(tt) - 1;  // the last tile that starts at or before o
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (q.before<Div>(mid, tt, group_log2) * kv_heads <= o) lo = mid; else hi = mid - 1;
+    }
+    const long long start = q.before<Div>(lo, tt, group_log2) * kv_heads;
+    const long long each_head = (long long)q.keys(lo, tt) * q.per_key<Div>(lo, tt, group_log2) + Div::ITEM;
+    tile = lo;
+    g = (int)((o - start) / each_head);
+    at = start + g * each_head;
+}
 
 // All NT threads of a CTA: sum the costs and place the walk at the CTA's
 // share.  `scratch` holds NT / 32 + 8 long longs of shared memory; the walk
@@ -249,22 +269,15 @@ __device__ __forceinline__ AttnWalk<Div> attn_walk_start(const AttnParams& p, lo
         for (int s = s0; s < s1; ++s) {
             AttnSeq q;
             q.load(p, s, false);
-            const int tiles = q.tiles(w.tt);
-            const long long c = q.before<Div>(tiles, w.tt, p.group_log2) * p.num_kv_heads;
+            const long long c = q.before<Div>(q.tiles(w.tt), w.tt, p.group_log2) * p.num_kv_heads;
             if (w.begin < pre + c) {
-                const long long o = w.begin - pre;
-                int lo = 0, hi = tiles - 1;  // the last tile that starts at or before o
-                while (lo < hi) {
-                    const int mid = (lo + hi + 1) >> 1;
-                    if (q.before<Div>(mid, w.tt, p.group_log2) * p.num_kv_heads <= o) lo = mid; else hi = mid - 1;
-                }
-                const long long start = q.before<Div>(lo, w.tt, p.group_log2) * p.num_kv_heads;
-                const long long each_head = (long long)q.keys(lo, w.tt) * q.per_key<Div>(lo, w.tt, p.group_log2) + Div::ITEM;
-                const int g = (int)((o - start) / each_head);
+                int tile, g;
+                long long at;
+                attn_place<Div>(q, w.tt, p.group_log2, p.num_kv_heads, w.begin - pre, tile, g, at);
                 scratch[NW + 1] = s;
-                scratch[NW + 2] = lo;
+                scratch[NW + 2] = tile;
                 scratch[NW + 3] = g;
-                scratch[NW + 4] = pre + start + g * each_head;
+                scratch[NW + 4] = pre + at;
                 scratch[NW + 5] = q.q0;
                 scratch[NW + 6] = q.n;
                 scratch[NW + 7] = q.valid ? q.first : -1;
@@ -287,6 +300,38 @@ __device__ __forceinline__ AttnWalk<Div> attn_walk_start(const AttnParams& p, lo
     w.q.n = (int)scratch[NW + 6];
     w.q.valid = scratch[NW + 7] >= 0;
     w.q.first = w.q.valid ? (int)scratch[NW + 7] : 0;
+    return w;
+}
+
+// The same start on the host, for CTA `cta` of `grid`; p's arrays are host ones.
+template <class Div>
+inline AttnWalk<Div> attn_walk_start_host(const AttnParams& p, int cta, int grid) {
+    AttnWalk<Div> w;
+    w.tt = Div::ROWS >> p.group_log2;
+    long long total = 0;
+    for (int s = 0; s < p.num_seqs; ++s) {
+        AttnSeq q;
+        q.load(p, s, false);
+        total += q.before<Div>(q.tiles(w.tt), w.tt, p.group_log2) * p.num_kv_heads;
+    }
+    w.share = (total + grid - 1) / grid;
+    if (w.share < 1) w.share = 1;
+    w.begin = w.share * cta;
+    w.end = w.begin + w.share < total ? w.begin + w.share : total;
+    long long pre = 0;
+    for (int s = 0; s < p.num_seqs; ++s) {
+        w.q.load(p, s, false);
+        const long long c = w.q.template before<Div>(w.q.tiles(w.tt), w.tt, p.group_log2) * p.num_kv_heads;
+        if (w.begin < pre + c) {
+            w.s = s;
+            attn_place<Div>(w.q, w.tt, p.group_log2, p.num_kv_heads, w.begin - pre, w.t, w.g, w.at);
+            w.at += pre;
+            return w;
+        }
+        pre += c;
+    }
+    w.at = w.end = w.begin;  // nothing to do
+    w.s = w.t = w.g = 0;
     return w;
 }
 
@@ -319,7 +364,7 @@ __device__ __forceinline__ void attn_check_parents(const AttnParams& p, const At
 // ------------------------------------------------------------------- merge
 // Partial result of part i of an item that CTA b owns: a CTA's first item may
 // go on from the CTA before (part > 0), its last may go on in the next.
-__device__ __forceinline__ int attn_partial(int b, int part) { return 2 * b + (part == 0 ? 1 : 0); }
+__host__ __device__ __forceinline__ int attn_partial(int b, int part) { return 2 * b + (part == 0 ? 1 : 0); }
 // Place in ws_o of dims d .. d + 3 of a partial result's row.
 __device__ __forceinline__ long long attn_partial_at(const AttnParams& p, int partial, int D, int d, int row) {
     return ((long long)partial * (D / 4) + d / 4) * p.part_rows + row;

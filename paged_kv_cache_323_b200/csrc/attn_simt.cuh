@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(256, 2) attn_simt_kernel(const AttnParams p) {
     AttnWalk<Div> walk = attn_walk_start<Div, C::THREADS>(p, walk_scratch);
     for (int n = 0;; ++n) {
         // the walk, by thread 0; a slot is written again only after the barrier of the item between
-        if (tid == 0 && !walk.next(p, item[n & 1])) item[n & 1].seq = -1;
+        if (tid == 0 && !walk.next(p, (int)blockIdx.x, item[n & 1])) item[n & 1].seq = -1;
         __syncwarp();
         __syncthreads();
         const AttnItem u = item[n & 1];

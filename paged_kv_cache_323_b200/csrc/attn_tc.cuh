@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 const uint32_t i = n & (C::ITEMS - 1);
                 if (n >= C::ITEMS && !wait(C::ITEM_EMPTY + 8 * i, (n / C::ITEMS - 1) & 1)) break;
                 AttnItem u;
-                const bool more = walk.next(p, u);
+                const bool more = walk.next(p, (int)blockIdx.x, u);
                 if (!more) u.seq = -1;
                 if (lane == 0) *reinterpret_cast<AttnItem*>(smem + C::ITEM_OFF + i * 64) = u;
                 arrive(C::ITEM_FULL + 8 * i);
@@ -1170,7 +1170,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             // counters end at zero and the others' results meet nothing stale
             AttnWalk<TcDivision> walk = *reinterpret_cast<const AttnWalk<TcDivision>*>(smem + C::WALK_OFF);
             int k = 0;
-            while (walk.next(p, u)) {
+            while (walk.next(p, (int)blockIdx.x, u)) {
                 const int n_rows = u.ntok << gl, first_row = n_rows > 128 ? warp * 32 : (warp & 3) * 32;
                 const bool few = u.nparts <= FEW_PARTS;
                 if (u.nparts == 1 || (few ? first_row >= n_rows || (n_rows <= 128 && warp >= 4) : warp > 0)) continue;
