@@ -781,8 +781,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             float qs = p.qscale;
             if constexpr (FP8) qs *= p.k_scales[u.g];
             // (a negative scale: the scores come negated.)  A scale of 0 weighs what is
-            // seen alike, and -inf * 0 is not -inf
-            const float qa = fmaxf(fabsf(qs), __uint_as_float(1u));
+            // seen alike, and -inf * 0 is not -inf; a scale of NaN stays one
+            const float qa = qs == 0.f ? __uint_as_float(1u) : fabsf(qs);
             const float2 q2 = make_float2(qa, qa);
             // keys that every row of the warp sees
             const int row0 = (plan.wide ? wg * 128 : 0) + (warp & 3) * 32;
