@@ -21,8 +21,8 @@
 // The reference m of a row's weights need not be its maximum, it cancels in
 // the quotient, and bf16 weights are as wide in range as fp32: m is the largest
 // of the first 32 scores that the row sees, and no other maximum is taken.
-// When the sum has passed 2^40 after a step, m, the sum and O are moved by its
-// power of two (hardly ever).
+// When weights take the sum past 2^40, m is raised past their scores, the sum
+// and O are moved by that, and the weights are taken again (hardly ever).
 //
 // Warps: 0-3 and 4-7 softmax, 8 producer (TMA: one 5-D copy brings a whole
 // block of K or V in the layout the MMA wants), 9 MMA issue, 10 the walk;
@@ -323,14 +323,14 @@ struct Cfg {
     static constexpr int RAW_OFF = SLOT_OFF + NSLOT * TILE;
     static constexpr int BAR_OFF = RAW_OFF + NRAW * RAW;
     // full/empty of the load ring, of the widened ring, q_full q_empty,
-    // s_full[2] p_full[2] p_rest[2] o_full[2], x_full x_empty, item full/empty, sync, mma_done
-    static constexpr int NBARS = 2 * NLOAD + (FP8 ? 2 * NSLOT : 0) + 2 + 8 + 2 + 2 * ITEMS + 2;
+    // s_full[2] p_full[2] p_rest[2] o_full[2] o_half[2], x_full x_empty, item full/empty, sync, mma_done
+    static constexpr int NBARS = 2 * NLOAD + (FP8 ? 2 * NSLOT : 0) + 2 + 10 + 2 + 2 * ITEMS + 2;
     static constexpr int LOAD_FULL = BAR_OFF, LOAD_EMPTY = LOAD_FULL + 8 * NLOAD;
     static constexpr int SLOT_FULL = FP8 ? LOAD_EMPTY + 8 * NLOAD : LOAD_FULL;  // what the MMA waits for
     static constexpr int SLOT_EMPTY = FP8 ? SLOT_FULL + 8 * NSLOT : LOAD_EMPTY;
     static constexpr int Q_FULL = SLOT_EMPTY + 8 * NSLOT, Q_EMPTY = Q_FULL + 8;
     static constexpr int S_FULL = Q_FULL + 16, P_FULL = S_FULL + 16, P_REST = S_FULL + 32, O_FULL = S_FULL + 48;
-    static constexpr int X_FULL = S_FULL + 64, X_EMPTY = X_FULL + 8;
+    static constexpr int O_HALF = S_FULL + 64, X_FULL = S_FULL + 80, X_EMPTY = X_FULL + 8;
     static constexpr int ITEM_FULL = X_EMPTY + 8, ITEM_EMPTY = ITEM_FULL + 8 * ITEMS;
     static constexpr int SYNC_BAR = ITEM_EMPTY + 8 * ITEMS, MMA_DONE = SYNC_BAR + 8;
     static_assert(MMA_DONE + 8 == BAR_OFF + NBARS * 8, "");
@@ -473,6 +473,82 @@ __device__ __noinline__ void slow_row(const AttnParams& p, const AttnItem& u, in
 #pragma unroll
         for (int x = 0; x < VE; ++x) acc[x] = fmaf(acc[x], a, w * static_cast<float>(v[x]) * vs);
     }
+}
+
+// Rows whose sum l_now with the weights of n more keys (32 or 64 scores at
+// t_x, `word` the seen ones of 32) has passed 2^40: a new reference at least as
+// large as those scores, moved by a power of two where that is within range, and what the
+// row has so far scaled to it: its sum l, O (t_o; ~0: nothing there yet) and, with
+// `scale_p`, the 16 columns of weights at t_p that no product has taken yet.
+// half: the barrier of the step's first product, which is waited for (0: none
+// in flight).  A row that sees an infinite score gets NaN as its sum.
+struct Raised {
+    float m, l;
+    bool ok;
+};
+template <int D>
+__device__ __noinline__ Raised raise(const AttnParams& p, uint32_t t_x, int n, uint32_t word, bool scale_p, uint32_t t_p,
+                                     uint32_t t_o, uint32_t half, uint32_t parity, volatile int* abort_flag, float qa,
+                                     float m, float l, float l_now) {
+    float mx = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < n; c += 32) {
+        float x[32];
+        tmem_ld32(t_x + c, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) x[e] = word & (1u << e) ? x[e] : -INFINITY;
+        mx = largest32(x, mx);
+    }
+    mx *= qa;
+    Raised r = {m, l, true};
+    float alpha = 1.f;
+    if (l > 0x1p40f) {
+        r.l = __uint_as_float(0x7fffffffu);  // raised in vain before
+    } else if (l_now > 0x1p40f) {
+        const float e = fmaxf(ceilf(mx - m), l > 1.f ? (float)((int)(__float_as_uint(l) >> 23) - 127) : 0.f);
+        if (e <= 126.f) {
+            alpha = __uint_as_float((uint32_t)(127 - (int)e) << 23);
+            r.m = m + e;
+        } else {  // nothing of the old sums is left
+            alpha = 0.f;
+            r.m = mx;
+        }
+        r.l = mx < INFINITY ? l * alpha : __uint_as_float(0x7fffffffu);
+    }
+    __syncwarp();
+    if (half != 0u && !(__all_sync(0xffffffffu, bar_test(half, parity)) ||
+                        bar_wait_slow(half, parity, abort_flag, p.wait_ns, p.err))) {
+        r.ok = false;
+        return r;
+    }
+    tc_fence_after();
+    if (t_o != ~0u) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(t_o + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= alpha;
+            tmem_st32(t_o + c, reinterpret_cast<const uint32_t*>(o));
+        }
+    }
+    if (scale_p) {
+        float x[32];
+        uint32_t* pk = reinterpret_cast<uint32_t*>(x);
+        tmem_ld32(t_p, x);
+        tmem_wait_ld();
+        const __nv_bfloat162 a = __float2bfloat162_rn(alpha);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&pk[e]), a);
+            pk[e] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+        tmem_st16(t_p, pk);
+    }
+    tmem_wait_st();
+    return r;
 }
 
 template <int D, bool FP8>
@@ -672,6 +748,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 for (int kk = 4 * part; kk < 4 * part + 4; ++kk)
                     mma_ts(tmem + C::O_COL + i * 128, tmem + i * 128 + kk * 8, b + ((kk * 2 * C::GSTRIDE) >> 4), v_hi,
                            C::IDESC_PV, kk > 0 ? 1u : accumulate, one);
+                if (part == 0) commit_one(sb + C::O_HALF + 8 * i, one);  // for raise()
             };
             AttnItem u;
             for (int n = 0; ok && take_item(n, u, ok); ++n) {
@@ -788,8 +865,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             const int row0 = (plan.wide ? wg * 128 : 0) + (warp & 3) * 32;
             const int clear = par ? u.first : u.pos + (row0 >> gl) + 1;
             float m = -INFINITY, l = 0.f;
-            float alpha_next = 1.f;  // what O is to be scaled by before the next product
-            bool stale = false;
             auto entry = [&](int t) {  // lane j: whether block j of step t is not in the pool
                 const int key = u.kv0 + plan.step(wg, t) * C::KEYS + lane * bs;
                 if (t >= nt || lane >= bpt || key >= u.kv1) return 0;
@@ -831,31 +906,30 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                         fence_proxy_async_smem();
                     }
                 }
-                auto rescale_o = [&](float alpha) {  // s_full: the product before this step's scores is complete
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        float o[32];
-                        tmem_ld32(t_o + c, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] *= alpha;
-                        tmem_st32(t_o + c, reinterpret_cast<const uint32_t*>(o));
-                    }
-                };
                 auto mask32 = [&](float* x, uint32_t word) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) x[e] = word & (1u << e) ? x[e] : -INFINITY;
                 };
-                if (stale) {
-                    rescale_o(alpha_next);
-                    stale = false;
-                }
-                float2 sum = make_float2(0.f, 0.f);
+                // Weights that take the sum past 2^40 are not used: the row's reference is raised first
+                // and they are taken again.  Once: where the reference's own rounding is that large
+                // (scores of 2^24 and more) the sum stays as it is, and the row is left to slow_row.
+                bool raised = false;
+                auto past = [&](float l_now) -> bool { return __any_sync(0xffffffffu, l_now > 0x1p40f) && !raised; };
+                auto lift = [&](float l_now, int c, int n, uint32_t word) {  // scores n c .. n c + n - 1 are in place
+                    const bool second = c * n >= 64;
+                    const Raised r = raise<D>(p, t_s + n * c, n, word, n == 32 && (c & 1), t_s + 16 * (c - 1),
+                                              t > 0 || second ? t_o : ~0u, second ? sb + C::O_HALF + 8 * wg : 0u,
+                                              s_phase ^ 1, abort_flag, qa, m, l, l_now);
+                    m = r.m;
+                    l = r.l;
+                    raised = true;
+                    return r.ok;
+                };
                 if (masked || (t > 0 && __any_sync(0xffffffffu, m == -INFINITY))) {
                     // steps with masks, in a short loop; of its 32 keys a warp's rows mostly see
                     // all or none
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < 4;) {
                         uint32_t pk[16];
                         const uint32_t word = !masked ? 0xffffffffu : c == 0 ? w[0] : c == 1 ? w[1] : c == 2 ? w[2] : w[3];
                         if (__any_sync(0xffffffffu, word != 0u)) {
@@ -869,65 +943,75 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                                 m = m == -INFINITY ? mx : m;
                             }
                             const float mm = m == -INFINITY ? 0.f : -m;
+                            float2 sum = make_float2(0.f, 0.f);
                             weights<32, false>(x, q2, make_float2(mm, mm), pk, sum);  // exactly 0 where masked
+                            const float l_now = l + (sum.x + sum.y);
+                            if (past(l_now)) {
+                                if (!(ok = lift(l_now, c, 32, word))) break;
+                                continue;
+                            }
+                            l = l_now;
+                            raised = false;
                         } else {
 #pragma unroll
                             for (int e = 0; e < 16; ++e) pk[e] = 0u;
                         }
                         tmem_st16(t_s + 16 * c, pk);  // over scores that have been read
-                        if (c == 1) {
+                        if (c & 1) {
                             tmem_wait_st();
                             if (!(ok = o_readable())) break;
                             tc_fence_before();
-                            arrive(C::P_FULL + 8 * wg);
+                            arrive((c == 1 ? C::P_FULL : C::P_REST) + 8 * wg);
                         }
+                        ++c;
                     }
                 } else {
                     // 64 keys at a time, in a loop: shorter code than the 128 in a row, which kept
                     // the roles waiting for instructions (4096 tokens of 16 heads: 102 us in a row,
                     // 97 in a loop)
+                    bool first = t == 0;
 #pragma unroll 1
-                    for (int c = 0; c < 2; ++c) {
+                    for (int c = 0; c < 2;) {
                         float x[64];
                         uint32_t pk[32];
                         tmem_ld32(t_s + 64 * c, x);
                         tmem_ld32(t_s + 64 * c + 32, x + 32);
                         tmem_wait_ld();
-                        if (t == 0 && c == 0) {
+                        if (first) {
+                            first = false;
                             m = largest32(x, -INFINITY) * qa;  // the row's reference
                             if (!(ok = o_readable())) break;
                         }
                         const float2 m2 = make_float2(-m, -m);
+                        float2 sum = make_float2(0.f, 0.f);
                         weights<32, !FP8>(x, q2, m2, pk, sum);
                         weights<32, !FP8>(x + 32, q2, m2, pk + 16, sum);
                         tmem_st32(t_s + 32 * c, pk);
-                        if (c == 0) {
+                        const float l_now = l + (sum.x + sum.y);
+                        tmem_wait_st();
+                        tc_fence_before();
+                        // (before the store, this look took 2 % more of a long prompt; scores that the
+                        // store went over have to go back)
+                        if (past(l_now)) {
+                            tmem_st32(t_s + 64 * c, reinterpret_cast<const uint32_t*>(x));
+                            tmem_st32(t_s + 64 * c + 32, reinterpret_cast<const uint32_t*>(x) + 32);
                             tmem_wait_st();
-                            tc_fence_before();
-                            arrive(C::P_FULL + 8 * wg);
+                            if (!(ok = lift(l_now, c, 64, 0xffffffffu))) break;
+                            continue;
                         }
+                        l = l_now;
+                        raised = false;
+                        // every lane's store is complete: each has waited for it before the vote
+                        if (lane == 0) bar_arrive(sb + (c == 0 ? C::P_FULL : C::P_REST) + 8 * wg);
+                        ++c;
                     }
                 }
                 if (!ok) break;
-                tmem_wait_st();
-                tc_fence_before();
-                arrive(C::P_REST + 8 * wg);
-                l += sum.x + sum.y;
-                if (__any_sync(0xffffffffu, !(l <= 0x1p40f))) {
-                    // NaN, infinite, or past what a weight can hold: for slow_row
-                    if (!(l <= 0x1p100f)) l = __uint_as_float(0x7fffffffu);
-                    if (t + 1 < nt) {
-                        const uint32_t e = l > 1.f ? (__float_as_uint(l) >> 23) - 127 : 0;  // l in [2^e, 2^(e + 1))
-                        alpha_next = __uint_as_float((127 - e) << 23);
-                        m += (float)e;
-                        l *= alpha_next;
-                        stale = true;  // O: once this step's product is complete
-                    }
-                }
             }
             if (!ok) break;
             base += 2 * plan.steps;
             if (m == -INFINITY) l = 0.f;  // no key seen
+            else if (l > 0x1p40f) l = __uint_as_float(0x7fffffffu);  // for slow_row
             // ------------------------------------------------ end of the item
             const float vs = FP8 ? p.v_scales[u.g] : 1.f;
             const bool two = !plan.wide && plan.n1 > 0;  // both pipelines hold parts of the same rows

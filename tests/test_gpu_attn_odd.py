@@ -1,5 +1,8 @@
 """Prompt and drafted-tree attention where a row's sums leave the ordinary
-range.  Compared with the plain 64-bit form."""
+range: cache scales that are not finite, scores that step up late in the
+context.  Compared with the plain 64-bit form; none of it may run into the
+kernels' time limit."""
+import copy
 import math
 
 import pytest
@@ -42,3 +45,98 @@ def test_cache_scales_that_are_not_finite(pk, tree, which, value, head_dim):
     ref, bound = attend(b, tree)
     assert not bool(torch.isfinite(ref[:, 4:]).any())
     close(got, ref, bound)
+
+
+def steps_up(b, at, unit=50.0):
+    """Scores near 0 for the first keys, `unit` more (powers of two of a weight) from each position of `at` on."""
+    b.q[..., 0] = 128.0
+    for s, (_, c) in enumerate(b.seqs):
+        pos = torch.arange(c, device="cuda")
+        blk = b.tables[s].long()[pos // b.bs]
+        level = sum((pos >= (a if a >= 0 else c + a)).float() for a in at) * unit
+        x = level / (128.0 * b.scale * 1.4426950408889634)
+        for h in range(b.G):
+            v = x / (b.ks[h] if b.ks is not None else 1.0)
+            cache = b.kc.view(torch.uint8) if b.dtype == "fp8" else b.kc
+            v = v.to(b.kc.dtype)
+            cache[blk, h, pos % b.bs, 0] = v.view(torch.uint8) if b.dtype == "fp8" else v
+
+
+@pytest.mark.parametrize("tree", [False, True], ids=["prefill", "tree"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "fp8"])
+@pytest.mark.parametrize("unit", [45.0, 120.0, 300.0])
+@pytest.mark.parametrize("seqs,heads,kv_heads,head_dim", [
+    ([(300, 1500), (257, 257)], 2, 1, 128),     # two tiles of rows at once
+    ([(40, 900), (9, 1200), (1, 400)], 4, 2, 128),  # even and odd steps of one tile
+    ([(5, 9000), (64, 3000)], 8, 2, 64),        # items in many and in few parts
+    ([(70, 700)] * 40, 4, 4, 64),               # whole items, several a CTA
+])
+def test_scores_that_step_up(pk, tree, dtype, unit, seqs, heads, kv_heads, head_dim):
+    """The reference of a row's weights, taken from its first keys, has to follow: by less and by more than
+    a weight can hold, in the first and in the second half of a step, in steps with and without masks."""
+    if dtype == "fp8" and unit == 300.0:
+        pytest.skip("past what e4m3 times its scale can hold")
+    for at in ((150,), (330,), (40, 650), (-30,), (100, -70)):
+        if dtype == "fp8" and unit == 120.0 and len(at) > 1:
+            continue
+        b = Batch(seqs, dtype=dtype, heads=heads, kv_heads=kv_heads, head_dim=head_dim, seed=61)
+        b.poison()
+        steps_up(b, at, unit)
+        got = b.call(pk, tree)
+        finish(pk)
+        ref, bound = attend(b, tree)
+        close(got, ref, bound, str(at))
+
+
+def long_items(dtype, keys, heads=296, rows=256, head_dim=64):
+    """One sequence whose every (tile, head) is a whole item of `keys` keys, two for a CTA: while the rows of
+    one are finished its other warps wait with the next.  The table goes round 64 blocks."""
+    bs = 32
+    b = Batch([(rows, 64 * bs)], dtype=dtype, heads=heads, kv_heads=heads, head_dim=head_dim, block_size=bs, seed=62)
+    b.tables = b.tables[:, :64].repeat(1, keys // (64 * bs)).contiguous()
+    b.seqs = [(rows, keys)]
+    b.ctx[0] = keys
+    return b
+
+
+def some_heads(b, n=2):
+    """The same batch with its first heads only."""
+    c = copy.copy(b)
+    c.H = c.G = n
+    c.q, c.kc, c.vc = b.q[:, :n], b.kc[:, :n].contiguous(), b.vc[:, :n].contiguous()
+    c.ks, c.vs = (b.ks[:n], b.vs[:n]) if b.ks is not None else (None, None)
+    return c
+
+
+def one_late_step(b):
+    """A block of its own at the end of the table but 4 blocks, whose keys' scores are some 2^120 times the others'."""
+    used = set(b.tables[0].tolist())
+    spare = next(i for i in range(b.kc.shape[0]) if i not in used)
+    b.tables[0, -12] = spare
+    b.q[..., 0] = 128.0
+    x = 120.0 / (128.0 * b.scale * 1.4426950408889634)
+    raw = b.kc.view(torch.uint8) if b.dtype == "fp8" else b.kc
+    raw[..., 0] = 0
+    v = torch.full((b.G,), x, device="cuda") / (b.ks if b.ks is not None else 1.0)
+    v = v.to(b.kc.dtype)
+    raw[spare, :, :, 0] = (v.view(torch.uint8) if b.dtype == "fp8" else v)[:, None]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("change", [one_late_step])
+@pytest.mark.parametrize("keys,limit_us", [(32768, 20000), (131072, 0)])
+def test_long_items_stay_within_the_time_limit(pk, dtype, change, keys, limit_us):
+    """Rows that need more work than others hold up the rest of their CTA, whose waits must not run out for it:
+    under the default limit, and under one that is far above any other wait of the call."""
+    b = long_items(dtype, keys)
+    change(b)
+    old = pk.set_wait_limit_us(limit_us)
+    try:
+        got = b.call(pk)
+        finish(pk)
+    finally:
+        pk.set_wait_limit_us(old)
+    c = some_heads(b)
+    ref, bound = attend(c)
+    close(got[:, :2], ref, bound)
+    assert bool(torch.isfinite(got).all())
