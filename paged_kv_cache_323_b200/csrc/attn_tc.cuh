@@ -33,8 +33,11 @@
 // sums and O are fp32.
 //
 // A masked key's weight is 0, and 0 * inf or 0 * nan would reach the row all
-// the same: rows whose result is not finite are computed again, key by key,
-// from the keys they see (slow_row).  Every wait is bounded.
+// the same, as would sums past fp32 of values near the largest: rows whose
+// result is not finite are computed again from the keys they see alone
+// (slow_rows: 148 tiles of 256 rows over 4096 keys take 21 ms of bf16 cache and
+// 37 ms of fp8 if every row goes that way, 0.11 and 0.12 ms if none does).
+// Every wait is bounded, by its own time and that of rows computed again.
 #pragma once
 
 #include <cuda.h>
@@ -96,18 +99,35 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity, uint32_t 
         : "memory");
     return ok != 0;
 }
+// Two of the CTA's words behind a shared-memory address: whether it has given
+// up, and when it last did work that others have to wait for (slow_rows; at
+// first its start).
+constexpr uint32_t ABORT = 8, BUSY_AT = 12;
+__device__ __forceinline__ void store_word(uint32_t at, uint32_t x) {
+    asm volatile("st.volatile.shared.b32 [%0], %1;" ::"r"(at), "r"(x) : "memory");
+}
+__device__ __forceinline__ uint2 load_words(uint32_t words) {
+    uint2 x;
+    asm volatile("ld.volatile.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(words + ABORT) : "memory");
+    return x;
+}
+__device__ __forceinline__ int short_time(unsigned long long ns) { return (int)(ns >> 10); }
 // Rest of a warp's wait whose first look was in vain: false when it ran out
-// of time or another warp has given up.
-__device__ __forceinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                           unsigned long long wait_ns, int* err) {
-    const unsigned long long t0 = globaltimer_ns();
+// of time or another warp has given up.  The time (in 1024 ns) runs from the
+// wait's start or from BUSY_AT, which rows that are computed again keep moving:
+// their loops end with the row's keys.
+__device__ __forceinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, uint32_t words, unsigned long long wait_ns,
+                                              int* err) {
+    const int t0 = short_time(globaltimer_ns());
     for (;;) {
         if (__all_sync(0xffffffffu, bar_try(bar, parity, 500u))) return true;
-        const bool late = globaltimer_ns() - t0 > wait_ns;
-        if (__any_sync(0xffffffffu, late || *abort_flag)) {
+        const int now = short_time(globaltimer_ns());
+        const uint2 w = load_words(words);
+        // differences are signed: another warp may have moved BUSY_AT past `now`
+        if (__any_sync(0xffffffffu, min(now - t0, now - (int)w.y) > short_time(wait_ns) || w.x != 0u)) {
             if ((threadIdx.x & 31) == 0) {
                 set_error(err, PKV_ERR_TIMEOUT);
-                *abort_flag = 1;
+                store_word(words + ABORT, 1u);
             }
             return false;
         }
@@ -334,7 +354,7 @@ struct Cfg {
     static constexpr int ITEM_FULL = X_EMPTY + 8, ITEM_EMPTY = ITEM_FULL + 8 * ITEMS;
     static constexpr int SYNC_BAR = ITEM_EMPTY + 8 * ITEMS, MMA_DONE = SYNC_BAR + 8;
     static_assert(MMA_DONE + 8 == BAR_OFF + NBARS * 8, "");
-    static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;  // tmem address, abort, flag, turns
+    static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;  // tmem address, flag, abort, busy at, turns
     static constexpr int ITEM_OFF = (MISC_OFF + 48 + 15) / 16 * 16;
     static constexpr int WALK_OFF = ITEM_OFF + ITEMS * 64;  // the CTA's walk, as it starts
     static constexpr int ML_OFF = WALK_OFF + 64;            // float2[128]; first the scratch of the walk's start
@@ -430,48 +450,138 @@ __device__ __forceinline__ void there_words(int count, uint32_t bad, int bs, uin
     }
 }
 
-// One row again, by one warp, from the keys it sees alone: what a row whose
-// result is not finite gets (a value of v outside the row's mask may have
-// reached it as 0 * inf).  Lanes hold D / 32 dims each; acc is not divided by l.
-template <int D, bool FP8>
-__device__ __noinline__ void slow_row(const AttnParams& p, const AttnItem& u, int r, float& m, float& l, float* acc) {
-    constexpr int VE = D / 32;
-    using TKV = typename std::conditional<FP8, __nv_fp8_e4m3, __nv_bfloat16>::type;
-    const int lane = threadIdx.x & 31;
+// Eight values of a cache row.
+template <bool FP8>
+__device__ __forceinline__ void load8(const void* cache, long long at, float* v) {
+    if constexpr (FP8) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const unsigned char*>(cache) + at));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __half2_raw h =
+                __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((i < 2 ? w.x : w.y) >> (16 * (i & 1))), __NV_E4M3);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
+    } else {
+        Elem<__nv_bfloat16>::unpack(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(cache) + at)), v);
+    }
+}
+
+// Rows again, SLOW at a time by one warp, from the keys they see alone: what
+// rows whose result is not finite get (a value of v outside a row's mask may
+// have reached it as 0 * inf).  32 keys at a time; a lane holds eight dims of
+// the rows, so D / 8 lanes read a key and the warp reads 2 or 4 keys at once;
+// sums of values stay apart by those until the end.  acc is not divided by l.
+// Meanwhile the CTA's other waits are put off (BUSY_AT).  One row at a time with a
+// key a lane took 70 and 61 ms where this takes 21 and 37.
+template <int SLOW>
+struct SlowRows {
+    int r[SLOW];  // rows of the item
+    float m[SLOW], l[SLOW], acc[SLOW][8];
+};
+template <int D, bool FP8, int SLOW>
+__device__ __noinline__ void slow_rows(const AttnParams& p, const AttnItem& u, uint32_t words, SlowRows<SLOW>& z) {
+    constexpr int LPR = D / 8;  // lanes that read a key
+    const int lane = threadIdx.x & 31, d0 = (lane & (LPR - 1)) * 8, group = lane & ~(LPR - 1);
     const int G = 1 << p.group_log2, bs = p.block_size;
-    const int i = u.pos - u.first + (r >> p.group_log2);
     const int32_t* par = p.parents ? p.parents + (u.row - (u.pos - u.first)) : nullptr;
     const int32_t* bt = p.block_tables + (long long)u.seq * p.max_blocks_per_seq;
     const float qs = FP8 ? p.qscale * p.k_scales[u.g] : p.qscale;
     const float vs = FP8 ? p.v_scales[u.g] : 1.f;
-    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) +
-                             (long long)(u.row + (r >> p.group_log2)) * p.q_stride + (u.g * G + (r & (G - 1))) * D +
-                             lane * VE;
-    float qv[VE];
+    float q[SLOW][8], acc[SLOW][8], m[SLOW], l[SLOW];
 #pragma unroll
-    for (int e = 0; e < VE; ++e) qv[e] = __bfloat162float(q[e]), acc[e] = 0.f;
-    m = -INFINITY;
-    l = 0.f;
-    for (int key = u.kv0; key < u.kv1; ++key) {
-        if (!sees(par, u.first, i, key)) continue;
-        const int e = bt[key / bs];
-        if (e < 0 || e >= p.num_blocks) continue;
-        const long long at = (((long long)e * p.num_kv_heads + u.g) * bs + key % bs) * D + lane * VE;
-        const TKV* k = static_cast<const TKV*>(p.k_cache) + at;
-        const TKV* v = static_cast<const TKV*>(p.v_cache) + at;
-        float s = 0.f;
+    for (int b = 0; b < SLOW; ++b) {
+        const int r = z.r[b];
+        load8<false>(p.q, (long long)(u.row + (r >> p.group_log2)) * p.q_stride + (u.g * G + (r & (G - 1))) * D + d0, q[b]);
+        m[b] = -INFINITY;
+        l[b] = 0.f;
 #pragma unroll
-        for (int x = 0; x < VE; ++x) s = fmaf(qv[x], static_cast<float>(k[x]), s);
+        for (int x = 0; x < 8; ++x) acc[b][x] = 0.f;
+    }
+#pragma unroll 1
+    for (int k0 = u.kv0; k0 < u.kv1; k0 += 32) {
+        if (lane == 0) store_word(words + BUSY_AT, short_time(globaltimer_ns()));
+        const int key = k0 + lane;
+        uint32_t seen[SLOW], any = 0u;
+        long long at = 0;  // the lane's key in the pools
+        bool there = false;
+        if (key < u.kv1) {
+            const int e = __ldg(bt + key / bs);
+            there = e >= 0 && e < p.num_blocks;
+            if (there) at = (((long long)e * p.num_kv_heads + u.g) * bs + key % bs) * D;
+        }
 #pragma unroll
-        for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        s *= qs;
-        const float mn = fmaxf(m, s);
-        const float a = mn == -INFINITY ? 1.f : exp2f(m - mn);
-        const float w = s == -INFINITY ? 0.f : exp2f(s - mn);
-        m = mn;
-        l = fmaf(l, a, w);
+        for (int b = 0; b < SLOW; ++b) {
+            seen[b] = __ballot_sync(0xffffffffu, there && sees(par, u.first, u.pos - u.first + (z.r[b] >> p.group_log2), key));
+            any |= seen[b];
+        }
+        if (any == 0u) continue;
+        float s[SLOW];
 #pragma unroll
-        for (int x = 0; x < VE; ++x) acc[x] = fmaf(acc[x], a, w * static_cast<float>(v[x]) * vs);
+        for (int b = 0; b < SLOW; ++b) s[b] = -INFINITY;
+#pragma unroll 4
+        for (int i = 0; i < LPR; ++i) {  // keys i, LPR + i, ..
+            const long long a = __shfl_sync(0xffffffffu, at, group + i);
+            float k[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (any >> (group + i) & 1u) load8<FP8>(p.k_cache, a + d0, k);
+#pragma unroll
+            for (int b = 0; b < SLOW; ++b) {
+                float dot = 0.f;
+#pragma unroll
+                for (int x = 0; x < 8; ++x) dot = fmaf(q[b][x], k[x], dot);
+#pragma unroll
+                for (int d = LPR / 2; d; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+                if (lane == group + i && (seen[b] >> lane & 1u)) s[b] = dot * qs;
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < SLOW; ++b) {
+            float mx = s[b];
+#pragma unroll
+            for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            const float mn = fmaxf(m[b], mx);
+            const float a = mn == -INFINITY ? 1.f : exp2f(m[b] - mn);
+            s[b] = s[b] == -INFINITY ? 0.f : exp2f(s[b] - mn);
+            float sum = s[b];
+#pragma unroll
+            for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            m[b] = mn;
+            l[b] = fmaf(l[b], a, sum);
+            s[b] *= vs;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) acc[b][x] *= a;
+        }
+#pragma unroll 4
+        for (int i = 0; i < LPR; ++i) {
+            const long long a = __shfl_sync(0xffffffffu, at, group + i);
+            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (any >> (group + i) & 1u) load8<FP8>(p.v_cache, a + d0, v);
+#pragma unroll
+            for (int b = 0; b < SLOW; ++b) {
+                const float w = __shfl_sync(0xffffffffu, s[b], group + i);
+                if (seen[b] >> (group + i) & 1u) {
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) acc[b][x] = fmaf(w, v[x], acc[b][x]);
+                }
+            }
+        }
+        bool done = true;  // NaN from here on
+#pragma unroll
+        for (int b = 0; b < SLOW; ++b) done = done && l[b] != l[b];
+        if (done) break;
+    }
+#pragma unroll
+    for (int b = 0; b < SLOW; ++b) {
+        z.m[b] = m[b];
+        z.l[b] = l[b];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            float o = acc[b][x];
+#pragma unroll
+            for (int d = LPR; d < 32; d <<= 1) o += __shfl_xor_sync(0xffffffffu, o, d);
+            z.acc[b][x] = l[b] == l[b] ? o : l[b];
+        }
     }
 }
 
@@ -488,8 +598,8 @@ struct Raised {
 };
 template <int D>
 __device__ __noinline__ Raised raise(const AttnParams& p, uint32_t t_x, int n, uint32_t word, bool scale_p, uint32_t t_p,
-                                     uint32_t t_o, uint32_t half, uint32_t parity, volatile int* abort_flag, float qa,
-                                     float m, float l, float l_now) {
+                                     uint32_t t_o, uint32_t half, uint32_t parity, uint32_t words, float qa,
+                                                                         float m, float l, float l_now) {
     float mx = -INFINITY;
 #pragma unroll 1
     for (int c = 0; c < n; c += 32) {
@@ -518,7 +628,7 @@ __device__ __noinline__ Raised raise(const AttnParams& p, uint32_t t_x, int n, u
     }
     __syncwarp();
     if (half != 0u && !(__all_sync(0xffffffffu, bar_test(half, parity)) ||
-                        bar_wait_slow(half, parity, abort_flag, p.wait_ns, p.err))) {
+                        bar_wait_slow(half, parity, words, p.wait_ns, p.err))) {
         r.ok = false;
         return r;
     }
@@ -560,8 +670,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t sb = smem_addr(smem);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
-    int* merge_flag = reinterpret_cast<int*>(smem + C::MISC_OFF + 8);
+    int* merge_flag = reinterpret_cast<int*>(smem + C::MISC_OFF + 4);
     int* turns = reinterpret_cast<int*>(smem + C::MISC_OFF + 16);  // [8] split items each softmax warp has counted
     float2* ml_x = reinterpret_cast<float2*>(smem + C::ML_OFF);
 
@@ -579,7 +688,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     }
     if (tid < 8) turns[tid] = 0;
     if (tid == 0) {
-        *abort_flag = 0;
+        store_word(sb + C::MISC_OFF + ABORT, 0u);
+        store_word(sb + C::MISC_OFF + BUSY_AT, short_time(globaltimer_ns()));
         for (const CUtensorMap* m : {&tmq, &tmk, &tmv})
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
     }
@@ -603,7 +713,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     // A wait by a converged warp; false: wind down.
     auto wait = [&](uint32_t off, uint32_t parity) -> bool {
         if (__all_sync(0xffffffffu, bar_test(sb + off, parity))) return true;
-        return bar_wait_slow(sb + off, parity, abort_flag, p.wait_ns, p.err);
+        return bar_wait_slow(sb + off, parity, sb + C::MISC_OFF, p.wait_ns, p.err);
     };
     auto arrive = [&](uint32_t off) {  // once for the warp, after what its lanes did
         __syncwarp();
@@ -912,14 +1022,14 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 };
                 // Weights that take the sum past 2^40 are not used: the row's reference is raised first
                 // and they are taken again.  Once: where the reference's own rounding is that large
-                // (scores of 2^24 and more) the sum stays as it is, and the row is left to slow_row.
+                // (scores of 2^24 and more) the sum stays as it is, and the row is left to slow_rows.
                 bool raised = false;
                 auto past = [&](float l_now) -> bool { return __any_sync(0xffffffffu, l_now > 0x1p40f) && !raised; };
                 auto lift = [&](float l_now, int c, int n, uint32_t word) {  // scores n c .. n c + n - 1 are in place
                     const bool second = c * n >= 64;
                     const Raised r = raise<D>(p, t_s + n * c, n, word, n == 32 && (c & 1), t_s + 16 * (c - 1),
                                               t > 0 || second ? t_o : ~0u, second ? sb + C::O_HALF + 8 * wg : 0u,
-                                              s_phase ^ 1, abort_flag, qa, m, l, l_now);
+                                              s_phase ^ 1, sb + C::MISC_OFF, qa, m, l, l_now);
                     m = r.m;
                     l = r.l;
                     raised = true;
@@ -1011,7 +1121,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             if (!ok) break;
             base += 2 * plan.steps;
             if (m == -INFINITY) l = 0.f;  // no key seen
-            else if (l > 0x1p40f) l = __uint_as_float(0x7fffffffu);  // for slow_row
+            else if (l > 0x1p40f) l = __uint_as_float(0x7fffffffu);  // for slow_rows
             // ------------------------------------------------ end of the item
             const float vs = FP8 ? p.v_scales[u.g] : 1.f;
             const bool two = !plan.wide && plan.n1 > 0;  // both pipelines hold parts of the same rows
@@ -1098,6 +1208,25 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 auto odd_rows = [&]() {
                     return __ballot_sync(0xffffffffu, here && nt > 0 && !(odd.x + odd.y == 0.f && l == l));
                 };
+                // Rows of this warp (bits) again; put(rows, which of them) by D / 8 lanes, with eight dims each.
+                constexpr int SLOW = FP8 ? 2 : 4;  // what the fp8 kernel's registers hold without spills
+                auto redo = [&](uint32_t again, auto&& put) {
+                    __syncwarp();
+                    while (again) {
+                        SlowRows<SLOW> z;
+#pragma unroll
+                        for (int b = 0; b < SLOW; ++b) {  // fewer rows than SLOW: the last one more than once
+                            z.r[b] = again ? row0 + __ffs(again) - 1 : z.r[b ? b - 1 : 0];
+                            again &= again - 1;
+                        }
+                        slow_rows<D, FP8, SLOW>(p, u, sb + C::MISC_OFF, z);
+                        if (lane < D / 8) {
+#pragma unroll 1
+                            for (int b = 0; b < SLOW; ++b) put(z, b);
+                        }
+                    }
+                    __syncwarp();
+                };
                 if (rows_left <= 0) {
                     // no rows of this warp
                 } else if (!split) {
@@ -1108,38 +1237,27 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                         look(o);
                         if (here) store32(dst + c, o);
                     }
-                    uint32_t again = odd_rows();
-                    __syncwarp();
-                    while (again) {
-                        const int r = row0 + __ffs(again) - 1;
-                        again &= again - 1;
-                        float ms, ls, acc[D / 32];
-                        slow_row<D, FP8>(p, u, r, ms, ls, acc);
+                    redo(odd_rows(), [&](const auto& z, int b) {
+                        const int r = z.r[b];
                         __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) +
                                             ((long long)(u.row + (r >> gl)) * p.num_heads + u.g * G + (r & (G - 1))) * D;
+                        uint32_t y[4];
 #pragma unroll
-                        for (int e = 0; e < D / 32; ++e)
-                            to[lane * (D / 32) + e] = __float2bfloat16_rn(ls == 0.f ? 0.f : acc[e] / ls);
-                    }
+                        for (int e = 0; e < 4; ++e)
+                            y[e] = z.l[b] == 0.f ? 0u : pack_bf16(z.acc[b][2 * e] / z.l[b], z.acc[b][2 * e + 1] / z.l[b]);
+                        reinterpret_cast<uint4*>(to)[lane] = make_uint4(y[0], y[1], y[2], y[3]);
+                    });
                 } else {
                     // With few parts each warp joins its own rows: the last of an item's parts to
                     // come has the others' results at hand and needs not write its own.
                     float4* to = p.ws_o + attn_partial_at(p, slot, D, 0, row);
                     float2* to_ml = p.ws_ml + (long long)slot * p.part_rows + row;
-                    auto redo = [&](uint32_t again) {  // rows of this part again, into the workspace
-                        __syncwarp();
-                        while (again) {
-                            const int r = row0 + __ffs(again) - 1;
-                            again &= again - 1;
-                            float ms, ls, acc[D / 32];
-                            slow_row<D, FP8>(p, u, r, ms, ls, acc);
-#pragma unroll
-                            for (int e = 0; e < D / 32; ++e)
-                                reinterpret_cast<float*>(p.ws_o + attn_partial_at(p, slot, D, lane * (D / 32), r))
-                                    [(lane * (D / 32)) % 4 + e] = acc[e];
-                            if (lane == 0) p.ws_ml[(long long)slot * p.part_rows + r] = make_float2(ms, ls);
-                        }
-                        __syncwarp();
+                    auto to_ws = [&](const auto& z, int b) {
+                        const int r = z.r[b];
+                        float4* to4 = p.ws_o + attn_partial_at(p, slot, D, 8 * lane, r);
+                        to4[0] = make_float4(z.acc[b][0], z.acc[b][1], z.acc[b][2], z.acc[b][3]);
+                        to4[p.part_rows] = make_float4(z.acc[b][4], z.acc[b][5], z.acc[b][6], z.acc[b][7]);
+                        if (lane == 0) p.ws_ml[(long long)slot * p.part_rows + r] = make_float2(z.m[b], z.l[b]);
                     };
                     int seen = 0;
                     if (few && lane == 0) asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(seen) : "l"(count) : "memory");
@@ -1161,7 +1279,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                         }
                         if (here) *to_ml = make_float2(m, l);
                         const uint32_t again = odd_rows();
-                        if (again) redo(again);
+                        redo(again, to_ws);
                     }
                     if (few) {
                         if (!last) {
@@ -1234,7 +1352,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                             const bool mine = !from_ws && nt > 0 && here && !(odd.x + odd.y == 0.f && l == l);
                             const uint32_t again = __ballot_sync(0xffffffffu, mine);
                             if (again == 0) break;
-                            redo(again);
+                            redo(again, to_ws);
                             from_ws = from_ws || mine;
                         }
                     }
@@ -1345,7 +1463,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (*abort_flag) {
+    if (load_words(sb + C::MISC_OFF).x != 0u) {
         // copies and products in flight land before the CTA leaves; each wait is bounded
         auto land = [&](uint32_t off, uint32_t parity) {
             const unsigned long long t0 = globaltimer_ns();

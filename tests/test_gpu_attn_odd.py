@@ -1,7 +1,7 @@
 """Prompt and drafted-tree attention where a row's sums leave the ordinary
 range: cache scales that are not finite, scores that step up late in the
-context.  Compared with the plain 64-bit form; none of it may run into the
-kernels' time limit."""
+context, values that are not finite in long contexts.  Compared with the plain
+64-bit form; none of it may run into the kernels' time limit."""
 import copy
 import math
 
@@ -88,6 +88,53 @@ def test_scores_that_step_up(pk, tree, dtype, unit, seqs, heads, kv_heads, head_
         close(got, ref, bound, str(at))
 
 
+SHAPES = [([(300, 700), (9, 60), (33, 33)], 4, 2), ([(5, 9000), (64, 3000)], 8, 2), ([(70, 700)] * 40, 4, 4),
+          ([(3, 200)] * 9, 8, 1)]
+
+
+@pytest.mark.parametrize("tree", [False, True], ids=["prefill", "tree"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "fp8"])
+@pytest.mark.parametrize("head_dim,block_size", [(128, 16), (64, 8), (128, 32)])
+@pytest.mark.parametrize("shape", range(len(SHAPES)))
+def test_values_that_are_not_finite(pk, tree, dtype, head_dim, block_size, shape):
+    """One value of v that is not finite, in a committed or a new token of some sequences: it reaches its dim of the
+    rows that see it; whole items, items in few and in many parts."""
+    seqs, heads, kv_heads = SHAPES[shape]
+    b = Batch(seqs, dtype=dtype, heads=heads, kv_heads=kv_heads, head_dim=head_dim, block_size=block_size, seed=63)
+    b.poison()
+    for s, (n, c) in enumerate(seqs):
+        if s % 3 == 2:
+            continue
+        pos = c - 1 - n // 2 if s % 3 else c // 3
+        blk, at, g = int(b.tables[s, pos // block_size]), pos % block_size, s % kv_heads
+        if dtype == "fp8":
+            b.vc.view(torch.uint8)[blk, g, at, 11] = 0x7F
+        else:
+            b.vc[blk, g, at, 11] = -math.inf if s % 2 else math.nan
+    got = b.call(pk, tree)
+    finish(pk)
+    ref, bound = attend(b, tree)
+    assert bool(torch.isfinite(ref).any()) and not bool(torch.isfinite(ref).all())
+    close(got, ref, bound)
+
+
+@pytest.mark.parametrize("tree", [False, True], ids=["prefill", "tree"])
+@pytest.mark.parametrize("head_dim", [128, 64])
+@pytest.mark.parametrize("shape", range(len(SHAPES)))
+def test_values_near_the_largest(pk, tree, head_dim, shape):
+    """Values of v whose sums with weights relative to the first keys pass what fp32 holds, the results do not."""
+    seqs, heads, kv_heads = SHAPES[shape]
+    b = Batch(seqs, dtype="bf16", heads=heads, kv_heads=kv_heads, head_dim=head_dim, seed=64)
+    b.vc *= 2.0 ** 110
+    b.poison()
+    steps_up(b, (60,), 32.0)
+    got = b.call(pk, tree)
+    finish(pk)
+    ref, bound = attend(b, tree)
+    assert bool(torch.isfinite(ref).all())
+    close(got, ref, bound)
+
+
 def long_items(dtype, keys, heads=296, rows=256, head_dim=64):
     """One sequence whose every (tile, head) is a whole item of `keys` keys, two for a CTA: while the rows of
     one are finished its other warps wait with the next.  The table goes round 64 blocks."""
@@ -108,6 +155,14 @@ def some_heads(b, n=2):
     return c
 
 
+def odd_value(b):
+    blk = int(b.tables[0, 0])
+    if b.dtype == "fp8":
+        b.vc.view(torch.uint8)[blk, :, 3, 5] = 0x7F
+    else:
+        b.vc[blk, :, 3, 5] = math.inf
+
+
 def one_late_step(b):
     """A block of its own at the end of the table but 4 blocks, whose keys' scores are some 2^120 times the others'."""
     used = set(b.tables[0].tolist())
@@ -123,7 +178,7 @@ def one_late_step(b):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp8"])
-@pytest.mark.parametrize("change", [one_late_step])
+@pytest.mark.parametrize("change", [odd_value, one_late_step])
 @pytest.mark.parametrize("keys,limit_us", [(32768, 20000), (131072, 0)])
 def test_long_items_stay_within_the_time_limit(pk, dtype, change, keys, limit_us):
     """Rows that need more work than others hold up the rest of their CTA, whose waits must not run out for it:
@@ -139,4 +194,8 @@ def test_long_items_stay_within_the_time_limit(pk, dtype, change, keys, limit_us
     c = some_heads(b)
     ref, bound = attend(c)
     close(got[:, :2], ref, bound)
-    assert bool(torch.isfinite(got).all())
+    if change is odd_value:
+        assert not bool(torch.isfinite(got[..., 5]).any())
+        assert bool(torch.isfinite(got[..., :5]).all()) and bool(torch.isfinite(got[..., 6:]).all())
+    else:
+        assert bool(torch.isfinite(got).all())
