@@ -1121,7 +1121,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             if (!ok) break;
             base += 2 * plan.steps;
             if (m == -INFINITY) l = 0.f;  // no key seen
-            else if (l > 0x1p40f) l = __uint_as_float(0x7fffffffu);  // for slow_rows
+            // The reference is a score that the row sees, or at most a power of two above one, and
+            // its weight in the sum: less (or more than 2^40) comes of scores whose rounding is
+            // larger than a weight's range.  For slow_rows, which rounds a score once.
+            else if (!(l >= 0.25f && l <= 0x1p40f)) l = __uint_as_float(0x7fffffffu);
             // ------------------------------------------------ end of the item
             const float vs = FP8 ? p.v_scales[u.g] : 1.f;
             const bool two = !plan.wide && plan.n1 > 0;  // both pipelines hold parts of the same rows

@@ -135,6 +135,55 @@ def test_values_near_the_largest(pk, tree, head_dim, shape):
     close(got, ref, bound)
 
 
+@pytest.mark.parametrize("tree", [False, True], ids=["prefill", "tree"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "fp8"])
+@pytest.mark.parametrize("log2_q", [17, 20, 34, 100])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_scores_past_their_own_rounding(pk, tree, dtype, log2_q, sign):
+    """Scores so large that fp32 rounds them by more than a weight's whole range: each row is the value of the
+    largest score that it sees.  Keys differ by 1/128 (fp8: by 2^-9 of the scale and more) and q is at least 2^17
+    (2^27), so scores of a row by at least 2^17 2^-7 log2(e) / sqrt(128) = 130 (2^27 2^-9 2^-5 0.127 = 1000)
+    powers of two."""
+    seqs = [(5, 100), (100, 100), (40, 90), (3, 3000), (1, 1)]
+    b = Batch(seqs, dtype=dtype, heads=4, kv_heads=2, seed=65)
+    b.scale *= sign
+    b.poison()
+    b.q.zero_()
+    b.q[..., 0] = sign * 2.0 ** (log2_q + (10 if dtype == "fp8" else 0))
+    raw = b.kc.view(torch.uint8) if dtype == "fp8" else b.kc
+    want = torch.empty(b.T, b.H, b.D, dtype=torch.float64, device="cuda")
+    gen = torch.Generator().manual_seed(65)
+    for s, (n, c) in enumerate(seqs):
+        order = (torch.arange(c) * 37) % 101 if c < 101 else torch.randint(0, 100, (c,), generator=gen)
+        if c >= 101:
+            order[c - n - 700] = 101
+        order = order.cuda()
+        pos = torch.arange(c, device="cuda")
+        blk, at = b.tables[s].long()[pos // b.bs], pos % b.bs
+        if dtype == "fp8":  # codes rise with their bits
+            raw[blk, :, at] = 0
+            raw[blk, :, at, 0] = (order + 8).to(torch.uint8)[:, None]
+        else:
+            raw[blk, :, at] = 0
+            raw[blk, :, at, 0] = (1 + order / 128.0).to(raw.dtype)[:, None]
+        for i in range(n):
+            seen = torch.arange(c, device="cuda") <= c - n + i
+            if tree:
+                seen = torch.arange(c, device="cuda") < c - n
+                j = i
+                while j >= 0:
+                    seen[c - n + j] = True
+                    j = int(b.parents[b.start_host[s] + j])
+            k = int(torch.where(seen, order, -1).argmax())
+            v = b.vc[blk[k], :, at[k]].double()
+            if dtype == "fp8":
+                v = v * b.vs.double()[:, None]
+            want[b.start_host[s] + i] = v.repeat_interleave(2, 0)
+    got = b.call(pk, tree).double()
+    finish(pk)
+    assert bool(((got - want).abs() <= 2.0 ** -7 * want.abs()).all())
+
+
 def long_items(dtype, keys, heads=296, rows=256, head_dim=64):
     """One sequence whose every (tile, head) is a whole item of `keys` keys, two for a CTA: while the rows of
     one are finished its other warps wait with the next.  The table goes round 64 blocks."""
