@@ -157,6 +157,7 @@ __global__ void __launch_bounds__(256, 2) attn_simt_kernel(const AttnParams p) {
             const int seen_by_all = p.parents ? u.first : u.pos + 1;
             const bool masked = bad || k0 + C::KEYS > (seen_by_all < u.kv1 ? seen_by_all : u.kv1);
             float alpha[R];
+            uint32_t unseen = 0u;  // a bit for each of the thread's scores
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 const int r = R * ty + i;
@@ -172,7 +173,10 @@ __global__ void __launch_bounds__(256, 2) attn_simt_kernel(const AttnParams p) {
                             const int e = bt[key / bs];
                             ok = e >= 0 && e < p.num_blocks;
                         }
-                        if (!ok) s[i][j] = -INFINITY;
+                        if (!ok) {
+                            s[i][j] = -INFINITY;
+                            unseen |= 1u << (4 * i + j);
+                        }
                     }
                     mx = fmaxf(mx, s[i][j]);
                 }
@@ -184,7 +188,7 @@ __global__ void __launch_bounds__(256, 2) attn_simt_kernel(const AttnParams p) {
                 float sum = 0.f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    // -inf scores (unseen keys) weigh zero whatever the maximum is
+                    // -inf scores weigh zero whatever the maximum is
                     s[i][j] = s[i][j] == -INFINITY ? 0.f : exp2f(s[i][j] - mn);
                     sum += s[i][j];
                 }
@@ -194,7 +198,8 @@ __global__ void __launch_bounds__(256, 2) attn_simt_kernel(const AttnParams p) {
 #pragma unroll
             for (int i = 0; i < R; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) sp[(R * ty + i) * C::LP + tx + 16 * j] = s[i][j];
+                for (int j = 0; j < 4; ++j)
+                    sp[(R * ty + i) * C::LP + tx + 16 * j] = unseen >> (4 * i + j) & 1u ? -1.f : s[i][j];
 #pragma unroll
             for (int i = 0; i < R; ++i)
 #pragma unroll
@@ -213,7 +218,7 @@ __global__ void __launch_bounds__(256, 2) attn_simt_kernel(const AttnParams p) {
 #pragma unroll
                         for (int i = 0; i < R; ++i) {
                             const float w = k == 0 ? a[i].x : k == 1 ? a[i].y : k == 2 ? a[i].z : a[i].w;
-                            if (masked && w == 0.f) continue;  // 0 * inf: an unseen key's V stays out
+                            if (masked && w < 0.f) continue;  // 0 * inf: an unseen key's V stays out, a seen one's does not
                             o[i][4 * j + 0] = fmaf(w, b.x, o[i][4 * j + 0]);
                             o[i][4 * j + 1] = fmaf(w, b.y, o[i][4 * j + 1]);
                             o[i][4 * j + 2] = fmaf(w, b.z, o[i][4 * j + 2]);

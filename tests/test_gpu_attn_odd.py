@@ -184,6 +184,22 @@ def test_scores_past_their_own_rounding(pk, tree, dtype, log2_q, sign):
     assert bool(((got - want).abs() <= 2.0 ** -7 * want.abs()).all())
 
 
+@pytest.mark.parametrize("tree", [False, True], ids=["prefill", "tree"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_value_of_a_weight_that_vanishes(pk, tree, dtype):
+    """A NaN value of a key that rows see with a weight below fp32's range reaches them, in steps with masks too."""
+    b = Batch([(40, 60), (3, 300), (9, 9)], dtype=dtype, heads=4, kv_heads=2, seed=66)
+    b.poison()
+    steps_up(b, (5,), 300.0)
+    for s in range(3):
+        b.vc[int(b.tables[s, 0]), :, 0, 7] = math.nan
+    got = b.call(pk, tree)
+    finish(pk)
+    ref, bound = attend(b, tree)
+    close(got, ref, bound)
+    assert bool(torch.isnan(got[:43, :, 7]).all())
+
+
 def long_items(dtype, keys, heads=296, rows=256, head_dim=64):
     """One sequence whose every (tile, head) is a whole item of `keys` keys, two for a CTA: while the rows of
     one are finished its other warps wait with the next.  The table goes round 64 blocks."""
