@@ -118,12 +118,21 @@ struct RopePiece<__nv_bfloat16> {
 // x / scale, correctly rounded, given r = 1 / scale correctly rounded: the
 // quotient's residual is exact in one fma, and one more rounds it (Markstein,
 // "Computation of elementary functions on the IBM RISC System/6000", 1990).
-// Infinities and NaN are those of x r; quotients too small for that are far
-// below the smallest code.
+// Infinities and NaN are those of x r, and a zero keeps its sign with the
+// residual taken this way round.  Holds for scales from 2^-90 to 2^100: r is a
+// normal number there, and where the residual is not exact (|x| below 2^-103)
+// the quotient is below 2^-13, the smallest code's half 2^-10.
 __device__ __forceinline__ float rope_quotient(float x, float scale, float r) {
     const float q = x * r;
-    const float y = fmaf(fmaf(-q, scale, x), r, q);
+    const float y = fmaf(-fmaf(q, scale, -x), r, q);
     return fabsf(q) < INFINITY ? y : q;
+}
+// Any other scale: values and scale times a power of two (or minus one) that
+// brings it there.  Values that overflow or lose bits by it have codes of 448
+// and 0 all the same.
+__device__ __forceinline__ float rope_factor(float scale) {
+    const float a = fabsf(scale);
+    return copysignf(a < 0x1p-90f ? 0x1p64f : a > 0x1p100f ? 0x1p-64f : 1.f, scale);
 }
 
 // Eight codes of value / scale, rounded to nearest even, saturated at 448.
@@ -238,13 +247,21 @@ __global__ void __launch_bounds__(kRopeThreads, 4) qk_rope_kernel(const RopePara
         Piece::unpack(*reinterpret_cast<const uint4*>(static_cast<const T*>(w) + d1), to + M);
     };
     // a row of a pool
-    auto store = [&](void* cache, const float* scales, int j, int g, const float2* x) {
+    auto store = [&](void* cache, const float* scales, int j, int g, float2* x) {
         const long long row = rows_at[j];
         if (row < 0 || !PKV_DCHECK(p.err, row + (long long)g * p.block_size < p.num_slots * Hkv && j < tokens)) return;
         const long long at = (row + (long long)g * p.block_size) * D;
         if constexpr (FP8) {
             uint8_t* to = static_cast<uint8_t*>(cache) + at;
-            const float scale = scales[g], r = __frcp_rn(scale);
+            float scale = scales[g];
+            if (!(scale >= 0x1p-90f && scale <= 0x1p100f)) {
+                const float f = rope_factor(scale);
+                scale *= f;
+#pragma unroll
+                for (int e = 0; e < 2 * M; ++e) x[e] = mul2(x[e], make_float2(f, f));
+            }
+            const float r = __frcp_rn(scale);
+            if (scale == INFINITY) scale = 1.f;  // (r = 0)
             *reinterpret_cast<uint2*>(to + d0) = rope_codes(x, scale, r);
             *reinterpret_cast<uint2*>(to + d1) = rope_codes(x + M, scale, r);
         } else {
