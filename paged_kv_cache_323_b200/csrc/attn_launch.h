@@ -11,8 +11,6 @@ namespace pkv {
 
 constexpr int kAttnSms = 148;
 
-// No grid is larger than two CTAs per SM: the workspace has counters for those.
-
 // What a launch asks of its workspace: CTAs of the grid (two partial results
 // each) and rows of a full tile.
 struct AttnShape {

@@ -10,10 +10,13 @@
 // rounding to the output's type (for an fp8 cache: of value / scale to e4m3).
 //
 // Angles.  fp32 has no room for them (at position 10^6 its spacing is 0.06), so
-// the product, exact in fp64 (a 24-bit by a 31-bit number), is brought into
-// [-pi, pi] there and only then rounded; the sine and cosine of a token's pairs
-// are computed once and serve all its heads.  With bf16 rows they come from
-// the special-function unit, within 2^-21: a thousandth of a bf16 step.
+// the product is taken in fp64, brought into [-pi, pi] there and only then
+// rounded; the sine and cosine of a token's pairs are computed once and serve
+// all its heads.  (The product is exact for positions below 2^29.  From there on
+// a 24-bit by a 31-bit number may need 55 bits where fp64 has 53: the farthest
+// angles are within 2^-22 radians at frequencies up to 1.)  With bf16 rows sine
+// and cosine come from the special-function unit, within 2^-21: a thousandth of
+// a bf16 step.
 //
 // Bound: HBM in bytes (one read of q, k, v and one write), and close behind it
 // the instructions of some 80 rows of 128 values a token.  A lane holds both
