@@ -300,9 +300,11 @@ PKV_API int qk_norm_rope_append_fp8(void* q_out, const void* q, const void* k, c
  *                included).  Two calls in flight at once, captured graphs
  *                included, must not share one, nor share it with a decode.
  * Otherwise as paged_attention_decode_ex.  A sequence with fewer context
- * tokens than queries, a context past its table, or rows outside q is a device
- * fault; its rows inside q become zeros.  A key that a row does not see has no
- * part in it, whatever its K and V hold.  One launch.
+ * tokens than queries or a context past its table is a device fault and its
+ * rows become zeros.  One whose rows do not all lie inside q, or run backwards,
+ * is a device fault too, and none of its rows is written, those inside q
+ * included.  A key that a row does not see has no part in it, whatever its K
+ * and V hold.  One launch.
  */
 PKV_API int paged_attention_prefill(void* out, const void* q, const void* k_cache, const void* v_cache,
                                     const int32_t* block_tables, const int32_t* context_lens,
