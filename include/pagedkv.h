@@ -293,7 +293,8 @@ PKV_API int qk_norm_rope_append_fp8(void* q_out, const void* q, const void* k, c
  *                query_start[num_seqs] to num_tokens, which pad the batch, may hold
  *                anything and stay as they are in out.
  *   q            [num_tokens][num_heads][head_dim], q_stride elements between
- *                two tokens (a multiple of 16 bytes); out is contiguous.
+ *                two tokens (a multiple of 16 bytes); out is contiguous and overlaps
+ *                none of the inputs (out == q: PKV_ERR_INVALID).
  *   workspace    at least paged_attention_prefill_workspace_size bytes,
  *                256-byte aligned, zero-filled once before its first use and
  *                left ready for the next call (of any shape, tree attention

@@ -481,6 +481,7 @@ int attn_impl(int kind, void* out, const void* q, const void* k_cache, const voi
     const AttnLayout w = attn_layout(num_tokens, group, head_dim, kv_dtype);
     if (workspace == nullptr || workspace_bytes < w.total || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
         return PKV_ERR_WORKSPACE;
+    if (out == q) return PKV_ERR_INVALID;  // rows computed again read q after their first result
     int dev = 0;
     if (current_device(&dev) != PKV_OK) return PKV_ERR_CUDA;
     int* err = nullptr;

@@ -505,7 +505,7 @@ def paged_attention_prefill(out, q, k_cache, v_cache, block_tables, context_lens
     """Causal attention of packed prompts, or chunks of them, whose K and V are
     in the cache: out, q [T][H][D] (q may be a slice over heads);
     query_start int32 [B + 1]; context_lens int32 [B] count the new tokens
-    too.  Rows from query_start[B] on are left as they are.  ``workspace``: a
+    too.  out must not overlap q.  Rows from query_start[B] on are left as they are.  ``workspace``: a
     zero-initialised uint8 CUDA tensor of at least
     :func:`paged_attention_prefill_workspace_size` bytes, or None for a buffer
     this module keeps per (device, stream): a call that is captured into a
