@@ -254,7 +254,7 @@ PKV_API int kv_cache_append(void* k_cache, void* v_cache, const void* k, const v
  *               [num_kv_heads][head_dim]; the strides are elements between two
  *               tokens, so all may be slices of one projection output
  *               (multiples of 16 bytes; heads of a token adjacent).  q_out may
- *               be q itself; it must not overlap anything else.
+ *               be q itself, with q's stride; it must not overlap anything else.
  *   positions   int32 [num_sections][num_tokens]; negative ones rotate back.
  *   inv_freq    float [R / 2].
  *   q_weight, k_weight  [head_dim] of `dtype`, or NULL.

@@ -554,6 +554,7 @@ int rope_impl(void* q_out, const void* q, const void* k, const void* v, void* k_
     for (int i = 0; i < 4; ++i)
         if (strides[i] < (long long)(i < 2 ? num_heads : num_kv_heads) * head_dim || strides[i] * eb % 16 != 0)
             return PKV_ERR_INVALID;
+    if (q_out == q && num_tokens > 1 && q_out_stride != q_stride) return PKV_ERR_INVALID;  // rows over other rows
     int dev = 0;
     if (current_device(&dev) != PKV_OK) return PKV_ERR_CUDA;
     int* err = nullptr;
