@@ -485,7 +485,7 @@ def _rope(name, q_out, q, k, v, k_cache, v_cache, scales, slot_mapping, position
              _ptr(inv_freq, "inv_freq", torch.float32, dev, (pairs,)),
              None if q_weight is None else _ptr(q_weight, "q_weight", act, dev, (D,)),
              None if k_weight is None else _ptr(k_weight, "k_weight", act, dev, (D,)),
-             eps, (_I * len(sections))(*sections), len(sections), 1 if interleaved else 0,
+             float(eps), (_I * len(sections))(*sections), len(sections), 1 if interleaved else 0,
              qo_s, q_s, k_s, v_s, T, H, Hkv, D, bs, N]
     if scales is None:
         args.append(_dtype_code(q))
@@ -576,7 +576,7 @@ def _attend(name, out, q, k_cache, v_cache, scales, block_tables, context_lens, 
         ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     else:
         ws_ptr, ws_bytes = _dev(workspace, "workspace", torch.uint8, device=dev), workspace.numel()
-    args += [q_stride, T, B, H, Hkv, D, bs, maxb, scale, N if num_blocks is None else int(num_blocks)]
+    args += [q_stride, T, B, H, Hkv, D, bs, maxb, float(scale), N if num_blocks is None else int(num_blocks)]
     if scales is None:
         args.append(_dtype_code(q))
     args += [ws_ptr, ws_bytes, st]
