@@ -112,6 +112,7 @@ __device__ __forceinline__ uint2 load_words(uint32_t words) {
     return x;
 }
 __device__ __forceinline__ int short_time(unsigned long long ns) { return (int)(ns >> 10); }
+constexpr unsigned long long UNHURRIED = 1ull << 40;  // 18 minutes
 // Rest of a warp's wait whose first look was in vain: false when it ran out
 // of time or another warp has given up.  The time (in 1024 ns) runs from the
 // wait's start or from BUSY_AT, which rows that are computed again keep moving:
@@ -711,9 +712,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     const int bl = 31 - __clz(bs);
 
     // A wait by a converged warp; false: wind down.
-    auto wait = [&](uint32_t off, uint32_t parity) -> bool {
+    auto wait = [&](uint32_t off, uint32_t parity, unsigned long long at_least = 0) -> bool {
         if (__all_sync(0xffffffffu, bar_test(sb + off, parity))) return true;
-        return bar_wait_slow(sb + off, parity, sb + C::MISC_OFF, p.wait_ns, p.err);
+        return bar_wait_slow(sb + off, parity, sb + C::MISC_OFF, at_least > p.wait_ns ? at_least : p.wait_ns, p.err);
     };
     auto arrive = [&](uint32_t off) {  // once for the warp, after what its lanes did
         __syncwarp();
@@ -740,7 +741,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             AttnWalk<TcDivision> walk = walk0;
             for (int n = 0;; ++n) {
                 const uint32_t i = n & (C::ITEMS - 1);
-                if (n >= C::ITEMS && !wait(C::ITEM_EMPTY + 8 * i, (n / C::ITEMS - 1) & 1)) break;
+                // (as long as an item takes, which may be any time: the other warps' waits end this one)
+                if (n >= C::ITEMS && !wait(C::ITEM_EMPTY + 8 * i, (n / C::ITEMS - 1) & 1, UNHURRIED)) break;
                 AttnItem u;
                 const bool more = walk.next(p, (int)blockIdx.x, u);
                 if (!more) u.seq = -1;

@@ -200,6 +200,25 @@ def test_value_of_a_weight_that_vanishes(pk, tree, dtype):
     assert bool(torch.isnan(got[:43, :, 7]).all())
 
 
+@pytest.mark.parametrize("tree", [False, True], ids=["prefill", "tree"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("head_dim", [128, 64])
+@pytest.mark.parametrize("seqs", [[(300, 900)], [(40, 900), (3, 500)], [(64, 3000)]])
+def test_large_values_of_vanishing_weights(pk, tree, dtype, head_dim, seqs):
+    """Values of 2^110 under weights of 2^-300: nothing of them is in the result."""
+    b = Batch(seqs, dtype=dtype, heads=4, kv_heads=2, head_dim=head_dim, seed=67)
+    b.poison()
+    steps_up(b, (64,), -300.0)
+    for s, (n, c) in enumerate(seqs):
+        pos = torch.arange(128, 384, device="cuda")
+        b.vc[b.tables[s].long()[pos // b.bs], :, pos % b.bs, 3] = 2.0 ** 110
+    got = b.call(pk, tree)
+    finish(pk)
+    ref, bound = attend(b, tree)
+    assert float(ref.abs().max()) < 10
+    close(got, ref, bound)
+
+
 def long_items(dtype, keys, heads=296, rows=256, head_dim=64):
     """One sequence whose every (tile, head) is a whole item of `keys` keys, two for a CTA: while the rows of
     one are finished its other warps wait with the next.  The table goes round 64 blocks."""
@@ -264,3 +283,22 @@ def test_long_items_stay_within_the_time_limit(pk, dtype, change, keys, limit_us
         assert bool(torch.isfinite(got[..., :5]).all()) and bool(torch.isfinite(got[..., 6:]).all())
     else:
         assert bool(torch.isfinite(got).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+def test_many_long_items_stay_within_the_time_limit(pk, dtype):
+    """Six items of 4M keys for each CTA: some 50 ms each, under a limit of 10 ms for a wait.  The table goes
+    round 64 blocks, so the result is that of 2048 keys; sums of 32768 steps are within 2^-9 of them each."""
+    b = long_items(dtype, 1 << 22, heads=148 * 6, rows=1)
+    old = pk.set_wait_limit_us(10000)
+    try:
+        got = b.call(pk)
+        finish(pk)
+    finally:
+        pk.set_wait_limit_us(old)
+    c = some_heads(b, 8)
+    c.tables, c.seqs = b.tables[:, :64], [(1, 2048)]
+    ref, bound = attend(c)
+    vmax = float((c.vc.float() * (c.vs.view(1, -1, 1, 1) if c.vs is not None else 1.0)).abs().max())
+    close(got[:, :8], ref, bound + 2.0 ** -8 * vmax)
+    assert bool(torch.isfinite(got).all())
