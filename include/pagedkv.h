@@ -261,7 +261,10 @@ PKV_API int kv_cache_append(void* k_cache, void* v_cache, const void* k, const v
  *   sections    host array: number of frequencies i of each position axis, in
  *               order (one axis: {R / 2}; time, height, width: three numbers).
  *               Their sum is R / 2, a multiple of 8, R <= head_dim; at most 4.
- * head_dim 64 or 128; any numbers of heads and block sizes.
+ * head_dim 64 or 128; any numbers of heads and block sizes.  Like the append's,
+ * the kernel releases a kernel launched next as a programmatic dependent at
+ * once; a caller's own such kernel must wait (griddepcontrol.wait) before it
+ * reads q_out or the pools.
  */
 PKV_API int qk_norm_rope_append(void* q_out, const void* q, const void* k, const void* v, void* k_cache,
                                 void* v_cache, const int64_t* slot_mapping, const int32_t* positions,
@@ -305,7 +308,8 @@ PKV_API int qk_norm_rope_append_fp8(void* q_out, const void* q, const void* k, c
  * rows become zeros.  One whose rows do not all lie inside q, or run backwards,
  * is a device fault too, and none of its rows is written, those inside q
  * included.  A key that a row does not see has no part in it, whatever its K
- * and V hold.  One launch.
+ * and V hold.  Sums of weight times value are fp32 and divided at the end, so
+ * |v| times the keys of a row must stay below 3.4e38.  One launch.
  */
 PKV_API int paged_attention_prefill(void* out, const void* q, const void* k_cache, const void* v_cache,
                                     const int32_t* block_tables, const int32_t* context_lens,

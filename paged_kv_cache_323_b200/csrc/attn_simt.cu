@@ -40,8 +40,10 @@ cudaError_t launch_inst(const AttnParams& p, cudaStream_t st) {
 AttnShape attn_simt_shape() { return AttnShape{kAttnSms * SimtCfg<64, 64>::CTAS_PER_SM, SimtCfg<64, 64>::ROWS}; }
 
 cudaError_t launch_attn_simt(const AttnParams& p, int D, cudaStream_t st) {
-    // few rows a sequence on average: small tiles, a quarter of the products each (two
-    // sequences of 3 and 5 drafts over 300 keys: 25 us against 34, both with cold caches)
+    // few rows a sequence on average: small tiles, a quarter of the products each.  64 sequences
+    // over 500 keys, small tiles against large: 65 against 98 us and 115 against 183 us at 16
+    // rows (2 and 4 kv heads), 213 against 184 us at 17, 105 against 101 us at 32.  (Two sequences
+    // over 300 keys leave most SMs idle and gain further up: 27 against 44 us at 32 rows.)
     if (((long long)p.num_tokens << p.group_log2) <= 16LL * p.num_seqs)
         return D == 64 ? launch_inst<64, 16>(p, st) : launch_inst<128, 16>(p, st);
     return D == 64 ? launch_inst<64, 64>(p, st) : launch_inst<128, 64>(p, st);

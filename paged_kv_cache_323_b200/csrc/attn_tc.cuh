@@ -57,8 +57,12 @@ using tc::tc_fence_after;
 using tc::tc_fence_before;
 using tc::tma_load_5d;
 
-// A step of 128 keys takes a full tile 3300 clocks; a tile of at most 128 rows, two steps
-// at a time, 2150 where K and V come from HBM; an item takes some 10000 besides.
+// Fitted over 1 to 6 items a CTA of 4 to 32 steps, caches cold, head_dim 128: a step
+// of 128 keys takes a full tile 2.05 us (fp8 2.5), a tile of at most 128 rows, two steps
+// at a time, 1.6 us (1.8) where K and V come from HBM; an item takes 5.4 us (5.0) or
+// 3.0 us (3.8) besides, a launch 14 us.  3 : 2 and three full steps an item are what
+// the calls gain by: 8192 tokens of 32 heads 567 -> 508 us, drafted trees over 128K
+// contexts 778 -> 672 us.
 using TcDivision = AttnDivision<256, 128, 2, 3, 128, 512, 1152>;
 
 // ------------------------------------------------------------ PTX wrappers
@@ -241,7 +245,8 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
 // 2^x of two values on the FMA pipe: x = n + f with n the nearest integer and
 // |f| <= 1/2, 2^f by the polynomial of degree 3 with the least relative error
 // there (an exchange algorithm's; 7.5e-5, a thirtieth of bf16's half step), n
-// added to the exponent.  Below -125 it gives 2^-125, above 127 and for NaN 2^127.
+// added to the exponent.  Below -125 it gives 2^-125 (of a value, next to the largest
+// weight of at least 2^-1: nothing that bf16 keeps), above 127 and for NaN 2^127.
 __device__ __forceinline__ float2 ex2_poly(float2 x) {
     x.x = fmaxf(fminf(x.x, 127.f), -125.f);
     x.y = fmaxf(fminf(x.y, 127.f), -125.f);
@@ -274,7 +279,9 @@ __device__ __forceinline__ void store_sector(void* to, const uint32_t (&r)[8]) {
 // total.  One pair in POLY_OF goes by ex2_poly, so that the special-function
 // unit (a quarter of the lanes a clock) and the FMA pipe share the work; not
 // over fp8 caches (952 us with it, 931 without, on 1024-token chunks over 15K
-// contexts), where widening is what keeps the pipes busy.
+// contexts), where widening is what keeps the pipes busy.  (4, 8, 16 and none
+// differ by less than runs do: 521, 522, 518, 515 us on 8192 tokens of 32 heads, and
+// 152 to 170 us each at head_dim 64 on 4096 tokens.)
 constexpr int POLY_OF = 8;
 template <int N, bool POLY>
 __device__ __forceinline__ void weights(const float* x, float2 q, float2 m, uint32_t* pk, float2& sum) {
@@ -366,7 +373,10 @@ struct Cfg {
 };
 
 // An item of at most this many parts is joined by the warps that have its
-// rows; more go over all threads (attn_merge).
+// rows; more go over all threads (attn_merge).  With 2: 50 against 46 us on prompts
+// behind a prefix (head_dim 64), 54 against 39 us on one prompt of 2048 tokens of 8 heads;
+// with 8: 79.5 against 77.5 us on packed prompts, 75 against 72 us on a batch of 64
+// drafted trees, though 49 against 65 us on two sequences of 64 queries over 3000 keys.
 constexpr int FEW_PARTS = 4;
 
 // What an item asks of the two pipelines.
