@@ -611,6 +611,7 @@ template <int D>
 __device__ __noinline__ Raised raise(const AttnParams& p, uint32_t t_x, int n, uint32_t word, bool scale_p, uint32_t t_p,
                                      uint32_t t_o, uint32_t half, uint32_t parity, uint32_t words, float qa,
                                                                          float m, float l, float l_now) {
+    tmem_wait_st();  // weights of the chunk before
     float mx = -INFINITY;
 #pragma unroll 1
     for (int c = 0; c < n; c += 32) {
